@@ -70,7 +70,8 @@ const char* q2_version(void);
  * current device recorded since the last check, and clears the record:
  * Q2_ERR_TIMEOUT if a bounded wait inside a kernel ran out (the tcgen05 GEMM
  * behind q2_linear), else Q2_ERR_INDEX if a kernel saw a token id outside
- * the vocabulary, else Q2_OK. */
+ * the vocabulary, else Q2_ERR_CAPACITY if a call on an 8-bit cache saw a
+ * length past max_seq, else Q2_OK. */
 q2_status q2_check_device_error(void* stream);
 
 /* Test hook: ORs `bits` (1: out-of-range id, 2: wait ran out) into the
@@ -186,6 +187,94 @@ q2_status q2_rope(void* out, const void* in, const int64_t* pos, size_t ntok, si
 q2_status q2_self_attention(void* out, const void* q, const void* k, const void* v, size_t seqlen,
                             size_t total_len, size_t nh, size_t nkv, size_t hd, float scale,
                             int dtype, void* stream);
+
+/* ---- 8-bit KV cache ------------------------------------------------------
+ * Codes of K and of V: [batch][nkv][max_seq][hd] bytes of e4m3 (16-byte
+ * aligned; hd in {32, 64, 128}).  Scales of each: fp32 [batch][nkv][nblk],
+ * nblk = ceil(max_seq / Q2_KV8_BLOCK): one per block of 64 positions and kv
+ * head; value = code * scale.  A scale is 2^k with the least k in [-60, 119]
+ * for which the largest finite magnitude of the block is at most 448 * 2^k.
+ * Magnitudes above 448 * 2^119 and infinities are held to it; a NaN is kept. */
+#define Q2_KV8_BLOCK 64
+
+/* kv8_append: writes ntok new rows of K and of V of each sequence at positions
+ * start[b] .. start[b] + ntok - 1 (start: device int32 [batch]; a negative
+ * start[b] marks an inactive sequence: nothing of it is touched).  k, v: fp32
+ * or bf16 [batch, ntok, nkv, hd]; the nkv * hd elements of a token are
+ * contiguous, k_strides / v_strides are HOST arrays {elements between
+ * sequences, elements between tokens} or NULL for dense.  A block whose first
+ * position is written gets a new scale; in a block that holds earlier
+ * positions the scale never falls, and where it grows the earlier codes are
+ * rounded to it.  Positions outside the written range keep their codes but for
+ * that.  start[b] + ntok past max_seq: nothing of that sequence is written and
+ * the device error word reports Q2_ERR_CAPACITY. */
+q2_status q2_kv8_append(void* kc, void* vc, float* ks, float* vs, const void* k, const void* v,
+                        const int64_t* k_strides, const int64_t* v_strides, const int32_t* start,
+                        size_t batch, size_t ntok, size_t nkv, size_t hd, size_t max_seq, int dtype,
+                        void* stream);
+
+/* kv8_read: k, v [batch, ntok, nkv, hd] (dense, `dtype`) = the cache's values
+ * at positions start[b] .. start[b] + ntok - 1.  Inactive sequences
+ * (start[b] < 0) and ranges past max_seq (Q2_ERR_CAPACITY in the device error
+ * word) leave their rows of k and v as they were. */
+q2_status q2_kv8_read(void* k, void* v, const void* kc, const void* vc, const float* ks,
+                      const float* vs, const int32_t* start, size_t batch, size_t ntok, size_t nkv,
+                      size_t hd, size_t max_seq, int dtype, void* stream);
+
+/* kv8_attention: causal GQA attention of the last ntok positions of each
+ * sequence over its 8-bit cache (append first).  lens: device int32 [batch],
+ * the positions held, the ntok new ones included; query row t of sequence b
+ * sees keys j <= lens[b] - ntok + t.  q [batch, ntok, nh, hd] (the nh * hd
+ * elements of a token contiguous; q_strides as k_strides above), out dense;
+ * scores, softmax and sums in fp32.  A row that sees no key (a sequence of
+ * length <= 0, or lens[b] < ntok) is zero; lens[b] past max_seq: zero rows and
+ * Q2_ERR_CAPACITY in the device error word.  Codes past lens[b] may hold
+ * anything.  nh / nkv <= 8.
+ * workspace: device memory of at least q2_kv8_attention_workspace() bytes,
+ * 256-byte aligned, contents ignored; calls that may overlap on the GPU need
+ * one each. */
+q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, const void* kc,
+                           const void* vc, const float* ks, const float* vs, const int32_t* lens,
+                           size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd,
+                           size_t max_seq, float scale, int dtype, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* kv8_self_attention: the same for a block of prompt rows of one sequence:
+ * q, out [seqlen, nh, hd] dense, kc, vc [nkv][max_seq][hd], ks, vs [nkv][nblk];
+ * query row i sees keys j <= total_len - seqlen + i.  The lengths are the
+ * host's. */
+q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const void* vc,
+                                const float* ks, const float* vs, size_t seqlen, size_t total_len,
+                                size_t nh, size_t nkv, size_t hd, size_t max_seq, float scale,
+                                int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The workspace that kv8_attention (total_len = 0) or kv8_self_attention
+ * (batch = 1, ntok = seqlen, total_len) needs on the current device, in
+ * *bytes. */
+q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len, size_t nh,
+                                     size_t nkv, size_t hd, int dtype, size_t* bytes);
+
+/* ---- 8-bit linear --------------------------------------------------------
+ * Operands in e4m3 with an fp32 scale per group of Q2_Q8_GROUP elements along
+ * the reduction: of one row (activations) or of 128 rows (weights).  With a =
+ * max(largest finite magnitude of the group, 2^-100): scale = a / 448, code =
+ * e4m3(x * (448 / a)), nearest even, held to +-448 (infinities too); a NaN is
+ * kept. */
+#define Q2_Q8_GROUP 128
+
+/* quantize_q8: in [rows, cols] (fp32 or bf16, in_stride elements between rows)
+ * -> codes [rows, cols] bytes and scales: block_rows == 1: [ceil(cols / 128)]
+ * [rows]; block_rows == 128: [ceil(rows / 128)][ceil(cols / 128)]. */
+q2_status q2_quantize_q8(void* codes, float* scales, const void* in, size_t rows, size_t cols,
+                         size_t in_stride, int block_rows, int dtype, void* stream);
+
+/* linear_q8: out[m, n] = sum over groups g of xs[g][m] * ws[n / 128][g] *
+ * (sum over k in g of xq[m, k] * wq[n, k]) + bias[n]; xq [M, K] and xs from
+ * quantize_q8 with block_rows 1, wq [N, K] and ws with block_rows 128, both
+ * codes 16-byte aligned, K a multiple of 16; bias [N] or NULL and out [M, N] in
+ * `dtype`; fp32 sums, one rounding. */
+q2_status q2_linear_q8(void* out, const void* xq, const float* xs, const void* wq, const float* ws,
+                       const void* bias, size_t M, size_t N, size_t K, int dtype, void* stream);
 
 /* swiglu: out[i] = up[i] * gate[i] / (1 + exp(-gate[i])), i < n. */
 q2_status q2_swiglu(void* out, const void* gate, const void* up, size_t n, int dtype,

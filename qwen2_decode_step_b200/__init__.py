@@ -22,7 +22,8 @@ __all__ = [
     "q2_argmax_noalloc", "q2_embedding", "q2_test_raise_device_error", "q2_test_attn_plan",
     "q2_test_gemm_tile",
     "q2_linear", "q2_test_tc_gemm", "q2_rms_norm", "q2_add_rms_norm", "q2_rope", "q2_self_attention", "q2_swiglu",
-    "q2_rearrange", "Model", "W_KIND", "STATUS", "KCLASS",
+    "q2_rearrange", "q2_kv8_append", "q2_kv8_read", "q2_kv8_attention", "q2_kv8_self_attention",
+    "q2_kv8_attention_workspace", "q2_quantize_q8", "q2_linear_q8", "KV8_BLOCK", "Q8_GROUP", "Model", "W_KIND", "STATUS", "KCLASS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -68,6 +69,14 @@ _SIGS = {
     "q2_self_attention": [_VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _SZ, _F, _I, _VP],
     "q2_swiglu": [_VP, _VP, _VP, _SZ, _I, _VP],
     "q2_rearrange": [_VP, _VP, _I, _VP, _VP, _VP, _SZ, _VP],
+    "q2_kv8_append": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _SZ, _I, _VP],
+    "q2_kv8_read": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _SZ, _I, _VP],
+    "q2_kv8_attention": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _F, _I, _VP, _SZ,
+                         _VP],
+    "q2_kv8_self_attention": [_VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _F, _I, _VP, _SZ, _VP],
+    "q2_kv8_attention_workspace": [_SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _I, ctypes.POINTER(_SZ)],
+    "q2_quantize_q8": [_VP, _VP, _VP, _SZ, _SZ, _SZ, _I, _I, _VP],
+    "q2_linear_q8": [_VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _I, _VP],
     "q2_model_create": [ctypes.POINTER(_Meta), _I, ctypes.POINTER(_VP)],
     "q2_model_destroy": [_VP],
     "q2_model_load_weight": [_VP, _I, _I, _VP, _SZ, _VP],
@@ -282,6 +291,179 @@ def q2_rearrange(out, inp, shape: Sequence[int], out_strides: Sequence[int],
     arr = ctypes.c_int64 * max(nd, 1)
     _call("q2_rearrange", _p(out), _p(inp), nd, arr(*shape), arr(*out_strides), arr(*in_strides),
           out.element_size(), _stream())
+    return out
+
+
+# ------------------------------------------------------- 8-bit cache and linear
+
+KV8_BLOCK = 64   # cache positions per scale
+Q8_GROUP = 128   # elements per scale along a linear's reduction
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _here(*ts):
+    """Every tensor on the current CUDA device (the stream of the call is its current stream)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else 0
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected tensors on the current CUDA device {dev}, got {t.device}")
+
+
+def _same_shape(what, *pairs):
+    for t, shape in pairs:
+        if t is not None and tuple(t.shape) != shape:
+            raise ValueError(f"{what}: expected a tensor of shape {shape}, got {tuple(t.shape)}")
+
+
+def _types(what, *pairs):
+    for t, dts in pairs:
+        if t is not None and t.dtype not in dts:
+            raise TypeError(f"{what}: expected {' or '.join(str(d) for d in dts)}, got {t.dtype}")
+
+
+def _cache8(what, kc, vc, ks, vs):
+    """The checks of a cache's four tensors; (batch, nkv, max_seq, hd)."""
+    _dense(kc, vc, ks, vs)
+    B, nkv, S, hd = kc.shape
+    _same_shape(what, (vc, (B, nkv, S, hd)), (ks, (B, nkv, -(-S // KV8_BLOCK))), (vs, (B, nkv, -(-S // KV8_BLOCK))))
+    _types(what, (kc, _E4M3), (vc, _E4M3), (ks, (torch.float32,)), (vs, (torch.float32,)))
+    return B, nkv, S, hd
+
+
+def _tok_strides(t):
+    """{between sequences, between tokens} of [batch, ntok, heads, hd] whose tokens are
+    contiguous (None: dense); anything else is refused."""
+    if t.is_contiguous():
+        return None
+    _, _, h, d = t.shape
+    if (d > 1 and t.stride(3) != 1) or (h > 1 and t.stride(2) != d):
+        raise ValueError("the heads of a token must be contiguous")
+    return (ctypes.c_int64 * 2)(t.stride(0), t.stride(1))
+
+
+def q2_kv8_append(kc, vc, ks, vs, k, v, start):
+    """Write k, v [batch, ntok, nkv, hd] (tokens contiguous, any token and sequence stride) at
+    positions start[b].. of the 8-bit cache: codes kc, vc [batch, nkv, max_seq, hd] (float8_e4m3fn
+    or uint8), scales ks, vs [batch, nkv, ceil(max_seq / 64)] fp32; start int32 [batch], negative =
+    inactive.  See q2.h."""
+    B, nkv, S, hd = _cache8("kv8_append", kc, vc, ks, vs)
+    T = k.shape[1]
+    _same_shape("kv8_append", (k, (B, T, nkv, hd)), (v, (B, T, nkv, hd)), (start, (B,)))
+    _types("kv8_append", (v, (k.dtype,)), (start, (torch.int32,)))
+    _dense(start)
+    _here(kc, vc, ks, vs, k, v, start)
+    _call("q2_kv8_append", kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.data_ptr(), v.data_ptr(),
+          _tok_strides(k), _tok_strides(v), start.data_ptr(), B, T, nkv, hd, S, _dtype(k), _stream())
+    return kc, vc, ks, vs
+
+
+def q2_kv8_read(k, v, kc, vc, ks, vs, start):
+    """k, v [batch, ntok, nkv, hd] = the cache's values at positions start[b].. (see q2.h)."""
+    B, nkv, S, hd = _cache8("kv8_read", kc, vc, ks, vs)
+    T = k.shape[1]
+    _same_shape("kv8_read", (k, (B, T, nkv, hd)), (v, (B, T, nkv, hd)), (start, (B,)))
+    _types("kv8_read", (v, (k.dtype,)), (start, (torch.int32,)))
+    _dense(k, v, start)
+    _here(kc, vc, ks, vs, k, v, start)
+    _call("q2_kv8_read", k.data_ptr(), v.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+          start.data_ptr(), B, T, nkv, hd, S, _dtype(k), _stream())
+    return k, v
+
+
+_ws_bytes: Dict[Tuple, int] = {}
+
+
+def q2_kv8_attention_workspace(batch, ntok, nh, nkv, hd, dtype=torch.bfloat16, total_len=0) -> int:
+    """Bytes of workspace that q2_kv8_attention (total_len = 0) or q2_kv8_self_attention
+    (batch = 1, ntok = its rows) needs on the current device."""
+    key = (torch.cuda.current_device(), batch, ntok, nh, nkv, hd, dtype, total_len)
+    n = _ws_bytes.get(key)
+    if n is None:
+        c = _SZ(0)
+        _call("q2_kv8_attention_workspace", batch, ntok, total_len, nh, nkv, hd, _DT[dtype], ctypes.byref(c))
+        if len(_ws_bytes) >= 4096:
+            _ws_bytes.clear()
+        n = _ws_bytes[key] = c.value
+    return n
+
+
+def _workspace(ws, dev, *args):
+    """The caller's workspace, or one from torch's allocator (stream-ordered, a graph's own)."""
+    if ws is None:
+        return torch.empty(q2_kv8_attention_workspace(*args), dtype=torch.uint8, device=dev)
+    _types("workspace", (ws, (torch.uint8,)))
+    _dense(ws)
+    _here(ws)
+    return ws
+
+
+def q2_kv8_attention(out, q, kc, vc, ks, vs, lens, scale, workspace=None):
+    """Causal attention of the last ntok positions of each sequence over its 8-bit cache: q, out
+    [batch, ntok, nh, hd] (q's tokens contiguous, any token and sequence stride), lens int32
+    [batch] (the new positions included).  See q2.h."""
+    B, nkv, S, hd = _cache8("kv8_attention", kc, vc, ks, vs)
+    _, T, nh, _ = q.shape
+    _same_shape("kv8_attention", (q, (B, T, nh, hd)), (out, (B, T, nh, hd)), (lens, (B,)))
+    _types("kv8_attention", (out, (q.dtype,)), (lens, (torch.int32,)))
+    _dense(out, lens)
+    _here(out, q, kc, vc, ks, vs, lens)
+    ws = _workspace(workspace, q.device, B, T, nh, nkv, hd, q.dtype)
+    _call("q2_kv8_attention", out.data_ptr(), q.data_ptr(), _tok_strides(q), kc.data_ptr(), vc.data_ptr(),
+          ks.data_ptr(), vs.data_ptr(), lens.data_ptr(), B, T, nh, nkv, hd, S, scale, _dtype(q), ws.data_ptr(),
+          ws.numel(), _stream())
+    return out
+
+
+def q2_kv8_self_attention(out, q, kc, vc, ks, vs, total_len, scale, workspace=None):
+    """The same for a block of prompt rows of one sequence: q, out [seqlen, nh, hd], kc, vc [nkv,
+    max_seq, hd], ks, vs [nkv, blocks]; row i sees keys j <= total_len - seqlen + i.  See q2.h."""
+    nkv, S, hd = kc.shape
+    T, nh, _ = q.shape
+    nb = -(-S // KV8_BLOCK)
+    _dense(out, q, kc, vc, ks, vs)
+    _same_shape("kv8_self_attention", (q, (T, nh, hd)), (out, (T, nh, hd)), (vc, (nkv, S, hd)), (ks, (nkv, nb)),
+                (vs, (nkv, nb)))
+    _types("kv8_self_attention", (out, (q.dtype,)), (kc, _E4M3), (vc, _E4M3), (ks, (torch.float32,)),
+           (vs, (torch.float32,)))
+    _here(out, q, kc, vc, ks, vs)
+    ws = _workspace(workspace, q.device, 1, T, nh, nkv, hd, q.dtype, total_len)
+    _call("q2_kv8_self_attention", out.data_ptr(), q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
+          vs.data_ptr(), T, total_len, nh, nkv, hd, S, scale, _dtype(q), ws.data_ptr(), ws.numel(), _stream())
+    return out
+
+
+def q2_quantize_q8(codes, scales, x, block_rows=1):
+    """x [rows, cols] (unit column stride) -> e4m3 codes [rows, cols] and fp32 scales: [ceil(cols /
+    128), rows] for block_rows 1 (activations), [ceil(rows / 128), ceil(cols / 128)] for 128
+    (weights).  See q2.h."""
+    rows, cols = x.shape
+    groups = -(-cols // Q8_GROUP)
+    _same_shape("quantize_q8", (codes, (rows, cols)),
+                (scales, (groups, rows) if block_rows == 1 else (-(-rows // 128), groups)))
+    _types("quantize_q8", (codes, _E4M3), (scales, (torch.float32,)))
+    _dense(codes, scales)
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError("the elements of a row must be contiguous")
+    _here(codes, scales, x)
+    _call("q2_quantize_q8", codes.data_ptr(), scales.data_ptr(), x.data_ptr(), rows, cols, x.stride(0), block_rows,
+          _dtype(x), _stream())
+    return codes, scales
+
+
+def q2_linear_q8(out, xq, xs, wq, ws, bias=None):
+    """out [M, N] (fp32 or bf16) = the product of quantised xq [M, K], xs [ceil(K / 128), M] and
+    wq [N, K], ws [ceil(N / 128), ceil(K / 128)] (+ bias [N] of out's dtype).  See q2.h."""
+    M, K = xq.shape
+    N = wq.shape[0]
+    groups = -(-K // Q8_GROUP)
+    _same_shape("linear_q8", (out, (M, N)), (xs, (groups, M)), (wq, (N, K)), (ws, (-(-N // 128), groups)),
+                (bias, (N,)))
+    _types("linear_q8", (xq, _E4M3), (wq, _E4M3), (xs, (torch.float32,)), (ws, (torch.float32,)),
+           (bias, (out.dtype,)))
+    _dense(out, xq, xs, wq, ws, bias)
+    _here(out, xq, xs, wq, ws, bias)
+    _call("q2_linear_q8", out.data_ptr(), xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+          None if bias is None else bias.data_ptr(), M, N, K, _dtype(out), _stream())
     return out
 
 

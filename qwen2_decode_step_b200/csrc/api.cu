@@ -63,8 +63,12 @@ q2_status device_error_status(int bits, const char* who) {
     set_error(msg);
     return Q2_ERR_TIMEOUT;
   }
-  set_error(msg + "a kernel saw a token id outside [0, vocab)");
-  return Q2_ERR_INDEX;
+  if (bits & kErrIndex) {
+    set_error(msg + "a kernel saw a token id outside [0, vocab)");
+    return Q2_ERR_INDEX;
+  }
+  set_error(msg + "a sequence's length is past the cache's max_seq");
+  return Q2_ERR_CAPACITY;
 }
 
 int num_sms() {

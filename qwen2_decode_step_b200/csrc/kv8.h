@@ -1,0 +1,28 @@
+// kv8.h -- internal launchers of the 8-bit KV cache.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/q2.h"
+
+namespace q2 {
+
+// Dequantised K and V rows of positions [start, start + ntok) of each sequence.
+struct Kv8Read {
+  void* k;
+  void* v;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const float* ks;
+  const float* vs;
+  const int32_t* start;  // [batch], or null: every sequence from position 0
+  long long seq_stride, tok_stride, head_stride;  // of k and v, in elements
+  int batch, ntok, nkv, hd, max_seq;
+  // With vnan (int [nkv][hd], zero): a NaN of V reads as 0 and vnan[g][d]
+  // becomes the largest INT32_MAX - position over the NaNs of that dimension.
+  int* vnan;
+};
+q2_status launch_kv8_read(const Kv8Read& a, int dtype, int* err, cudaStream_t st);
+
+}  // namespace q2
