@@ -26,15 +26,15 @@ EncodeTiledFn encode_fn() {
 }
 }  // namespace
 
-q2_status make_tmap_2d_bf16(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
-                            uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols,
-                            int swizzle_bytes) {
+static q2_status make_tmap_2d(CUtensorMap* out, CUtensorMapDataType type, uint32_t elem, const void* base,
+                              uint64_t rows, uint64_t cols, uint64_t pitch_bytes, uint32_t box_rows,
+                              uint32_t box_cols, int swizzle_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) {
     set_error("cuTensorMapEncodeTiled is not available");
     return Q2_ERR_CUDA;
   }
-  if ((reinterpret_cast<uintptr_t>(base) & 15) || (pitch_bytes & 15) || ((box_cols * 2) & 15)) {
+  if ((reinterpret_cast<uintptr_t>(base) & 15) || (pitch_bytes & 15) || ((box_cols * elem) & 15)) {
     set_error("tensor map: base, pitch and box width must be 16-byte multiples");
     return Q2_ERR_INVALID_ARG;
   }
@@ -46,7 +46,7 @@ q2_status make_tmap_2d_bf16(CUtensorMap* out, const void* base, uint64_t rows, u
                           : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                           : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                 : CU_TENSOR_MAP_SWIZZLE_NONE;
-  CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+  CUresult r = fn(out, type, 2, const_cast<void*>(base), dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
@@ -54,6 +54,19 @@ q2_status make_tmap_2d_bf16(CUtensorMap* out, const void* base, uint64_t rows, u
     return Q2_ERR_CUDA;
   }
   return Q2_OK;
+}
+
+q2_status make_tmap_2d_bf16(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
+                            uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols,
+                            int swizzle_bytes) {
+  return make_tmap_2d(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols, pitch_bytes, box_rows, box_cols,
+                      swizzle_bytes);
+}
+
+q2_status make_tmap_2d_u8(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
+                          uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols, int swizzle_bytes) {
+  return make_tmap_2d(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, cols, pitch_bytes, box_rows, box_cols,
+                      swizzle_bytes);
 }
 
 }  // namespace q2

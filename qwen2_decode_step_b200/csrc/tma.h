@@ -17,9 +17,14 @@ q2_status make_tmap_2d_bf16(CUtensorMap* out, const void* base, uint64_t rows, u
                             uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols,
                             int swizzle_bytes);
 
+// The same for bytes (e4m3 codes): box_cols bytes wide.
+q2_status make_tmap_2d_u8(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
+                          uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols,
+                          int swizzle_bytes);
+
 // Tiled 2-D TMA load of one box at (x = column, y = row) into shared memory,
 // completing on `bar` (transaction bytes).  The column coordinate must be a
-// multiple of 8 for bf16 (16-byte alignment of the innermost coordinate);
+// multiple of 8 for bf16, of 16 for bytes (16-byte alignment of the innermost coordinate);
 // rows beyond the tensor read as zeros.  No multicast.
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
