@@ -21,10 +21,13 @@
 //         two-lane FMA per two products and no operand but registers (with the
 //         weights on the lanes every column would need its own scale from
 //         shared memory).
-// Warp roles (320 threads, one CTA per SM, persistent over the tiles): warp 0
+// Warp roles (384 threads, one CTA per SM, persistent over the tiles): warp 0
 // TMA (a 128 x 128-byte and a BN x 128-byte box per group, 128-byte swizzle, a
-// ring of STAGES), warp 1 tensor memory and MMA, warps 2-9 epilogue: two per
-// TMEM lane quarter, each half of the columns.
+// ring of STAGES), warp 1 tensor memory and MMA, warps 4-11 epilogue: two per
+// TMEM lane quarter, each half of the columns.  The first four warps give most
+// of their registers to the epilogue's: a wide thread keeps 128 sums and takes
+// 64 products of a group per TMEM load (32 at a time left the loads' latency
+// bare: 1470 cycles per group instead of the MMA's 512).
 // When the tiles alone leave SMs idle, a cluster of up to 8 CTAs splits the
 // groups of one tile: each leaves its fp32 partial tile in its shared memory
 // and every CTA adds one share of it over the cluster in rank order
@@ -33,8 +36,6 @@
 // Every wait is bounded: one that runs out sets value 2 in the device error
 // word and the kernel carries on to its end.
 #include <cooperative_groups.h>
-
-#include <atomic>
 
 #include "common.cuh"
 #include "e4m3.cuh"
@@ -50,7 +51,11 @@ namespace {
 constexpr int kGroup = Q2_Q8_GROUP;
 constexpr int kLanes = 128;                 // rows of the lane-side operand per tile
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kEpiWarp0 = 4;                // warps 2 and 3 only fill their warpgroup
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+// registers: launched with 168 a thread (64512 / 384); the first warpgroup
+// drops to 40, the two of the epilogue rise to 232: 128 * 40 + 256 * 232 = 64512
+constexpr int kRegsLow = 40, kRegsHigh = 232;
 constexpr int kClusterMax = 8;
 
 struct Q8Lin {
@@ -59,11 +64,10 @@ struct Q8Lin {
   const void* bias;   // [N] or null
   void* out;          // [M][N]
   int M, N, groups;
-  int out_f32;
   int lane_tiles, tiles;  // of the lane-side operand; of the output
   int csize;          // CTAs that share a tile
   int g_per;          // groups per CTA of a cluster
-  int vec;            // rows of out start on 16 bytes
+  int tma_out;        // wide: the output's tensor map is valid
   int* err;
 };
 
@@ -82,34 +86,37 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// NC consecutive fp32 columns (8, 16 or 32) of this thread's TMEM lane.
+// NC consecutive columns (8, 16 or 32) of this thread's TMEM lane, as bits; the
+// values may be used after tmem_wait.
 template <int NC>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
   if constexpr (NC == 32) {
-    tmem_ld32(taddr, v);
-  } else if constexpr (NC == 16) {
-    uint32_t r[16];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+  } else if constexpr (NC == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
   } else {
-    uint32_t r[8];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr));
   }
 }
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-template <int BN, int STAGES>
+template <bool WIDE, int BN, int STAGES>
 struct Q8Smem {
   static constexpr size_t kA = (size_t)kLanes * kGroup;
   static constexpr size_t kB = (size_t)BN * kGroup;
@@ -118,33 +125,56 @@ struct Q8Smem {
   static constexpr int kAcc = BN > 128 ? 2 : 4;
   static constexpr int kCols = kAcc * BN <= 64 ? 64 : kAcc * BN <= 128 ? 128 : kAcc * BN <= 256 ? 256 : 512;
   static constexpr size_t kBars = (2 * STAGES + 2 * kAcc) * 8 + 16;
-  static constexpr size_t kTotal = STAGES * kStage + kBars + 1024;  // + alignment slack
-  // a cluster's partial tile, [column][lane], lanes padded to an odd stride so
-  // that it can be walked along either axis
-  static constexpr int kPartStride = kLanes + 1;
-  static constexpr bool kFits = (size_t)BN * kPartStride * 4 <= STAGES * kStage;
+  // wide: 32 rows x 128 bytes of output per epilogue warp, to turn them
+  static constexpr size_t kTurn = STAGES * kStage;
+  static constexpr size_t kBarOff = kTurn + (WIDE ? kEpiWarps * 4096 : 0);
+  static constexpr size_t kTotal = kBarOff + kBars + 1024;  // + alignment slack
+  // a cluster's partial tile, features contiguous (distributed shared memory
+  // moves neighbouring words together): wide [token lane][BN], rows 16 bytes
+  // longer against bank conflicts of the writes; tall [token column][lane]
+  static_assert(kTotal <= 232448, "shared memory of one CTA");
+  static constexpr int kPartStride = WIDE ? BN + 4 : kLanes;
+  static constexpr bool kFits = (size_t)(WIDE ? kLanes : BN) * kPartStride * 4 <= STAGES * kStage;
 };
 
-__device__ __forceinline__ void store_out(const Q8Lin& a, int m, int n, float y) {
-  const size_t i = (size_t)m * a.N + n;
-  if (a.out_f32) {
-    if (a.bias) y += reinterpret_cast<const float*>(a.bias)[n];
-    reinterpret_cast<float*>(a.out)[i] = y;
-  } else {
-    if (a.bias) y += to_f(reinterpret_cast<const bf16*>(a.bias)[n]);
-    reinterpret_cast<bf16*>(a.out)[i] = from_f<bf16>(y);
-  }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// ta: the lane-side operand's map, tb: the column-side one's.
-template <bool WIDE, int BN, int STAGES>
+template <typename T>
+__device__ __forceinline__ void store_out(const Q8Lin& a, int m, int n, float y) {
+  if (a.bias) y += to_f(reinterpret_cast<const T*>(a.bias)[n]);
+  reinterpret_cast<T*>(a.out)[(size_t)m * a.N + n] = from_f<T>(y);
+}
+
+// A CTA's tiles in order (first, first + step, ...): lane-side tile lt fastest.
+struct TileWalk {
+  int t, lt, ct, step, dl, dc, lane_tiles;
+  __device__ __forceinline__ TileWalk(int first, int step_, int lane_tiles_)
+      : t(first), lt(first % lane_tiles_), ct(first / lane_tiles_), step(step_), dl(step_ % lane_tiles_),
+        dc(step_ / lane_tiles_), lane_tiles(lane_tiles_) {}
+  __device__ __forceinline__ void next() {
+    t += step;
+    lt += dl;
+    ct += dc;
+    if (lt >= lane_tiles) {
+      lt -= lane_tiles;
+      ++ct;
+    }
+  }
+};
+
+// ta: the lane-side operand's map, tb: the column-side one's, to: the output's
+// (wide, boxes of 32 tokens x 128 bytes).
+template <typename T, bool WIDE, int BN, int STAGES>
 __global__ void __launch_bounds__(kThreads, 1)
-    q8_linear_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, const Q8Lin a) {
-  using SM = Q8Smem<BN, STAGES>;
+    q8_linear_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                     const __grid_constant__ CUtensorMap to, const Q8Lin a) {
+  using SM = Q8Smem<WIDE, BN, STAGES>;
   static_assert(SM::kFits && SM::kAcc * BN <= 512, "the partial tile fits the ring, the accumulators tensor memory");
   extern __shared__ __align__(1024) uint8_t q8_smem_raw[];
   uint8_t* smem = q8_smem_raw + ((1024u - (smem_u32(q8_smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * SM::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBarOff);
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + SM::kAcc;
@@ -179,45 +209,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_launch_dependents();
   pdl_wait();  // codes and scales may be the kernel before's
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      for (int t = first; t < a.tiles; t += step) {
-        const int r0 = (t % a.lane_tiles) * kLanes, c0 = (t / a.lane_tiles) * BN;
-        for (int g = g0; g < g1; ++g) {
-          uint8_t* st = smem + s * SM::kStage;
-          if (!tc_wait(&empty[s], ph ^ 1u)) atomicOr(a.err, kErrTimeout);
-          mbar_arrive_expect_tx(&full[s], (uint32_t)SM::kStage);
-          tma_load_2d(st, &ta, g * kGroup, r0, &full[s]);
-          tma_load_2d(st + SM::kA, &tb, g * kGroup, c0, &full[s]);
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
+  // (setmaxnreg inside each branch: the compiler allots a joint path the lower
+  // count)
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
+    if (warp == 0) {
+      // ------------------------------------------------------------ producer
+      if (lane == 0) {
+        int s = 0;
+        uint32_t ph = 0;
+        for (TileWalk w(first, step, a.lane_tiles); w.t < a.tiles; w.next()) {
+          const int r0 = w.lt * kLanes, c0 = w.ct * BN;
+          for (int g = g0; g < g1; ++g) {
+            uint8_t* st = smem + s * SM::kStage;
+            if (!tc_wait_asleep(&empty[s], ph ^ 1u)) atomicOr(a.err, kErrTimeout);
+            mbar_arrive_expect_tx(&full[s], (uint32_t)SM::kStage);
+            tma_load_2d(st, &ta, g * kGroup, r0, &full[s]);
+            tma_load_2d(st + SM::kA, &tb, g * kGroup, c0, &full[s]);
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
           }
         }
       }
-    }
-  } else if (warp == 1) {
-    // ----------------------------------------------------------------- MMA
-    if (lane == 0) {
+    } else if (warp == 1) {
+      // ----------------------------------------------------------------- MMA
+      // The whole warp walks the loop and one elected lane issues, so that the
+      // descriptors stay in uniform registers (from one lane's own registers a
+      // group's six instructions took 400 cycles to issue).
       constexpr uint32_t idesc = idesc_e4m3(BN);
+      const uint64_t da0 = sw128_desc(smem), db0 = sw128_desc(smem + SM::kA);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       for (int t = first; t < a.tiles; t += step) {
         for (int g = g0; g < g1; ++g) {
-          if (!tc_wait(&acc_empty[acc], aph ^ 1u)) atomicOr(a.err, kErrTimeout);
-          if (!tc_wait(&full[s], ph)) atomicOr(a.err, kErrTimeout);
+          if (!tc_wait_asleep(&acc_empty[acc], aph ^ 1u) && lane == 0) atomicOr(a.err, kErrTimeout);
+          if (!tc_wait_asleep(&full[s], ph) && lane == 0) atomicOr(a.err, kErrTimeout);
           tc_fence_after();
-          const uint8_t* st = smem + s * SM::kStage;
-          const uint64_t da = sw128_desc(st), db = sw128_desc(st + SM::kA);
-          const uint32_t d = tmem + (uint32_t)(acc * BN);
+          if (elect_one()) {
+            const uint64_t at = (uint64_t)((uint32_t)s * (uint32_t)(SM::kStage >> 4));
+            const uint32_t d = tm + (uint32_t)(acc * BN);
 #pragma unroll
-          for (int k = 0; k < kGroup / 32; ++k)  // 32 bytes along the swizzle atom
-            mma_e4m3(d, da + (uint64_t)(2 * k), db + (uint64_t)(2 * k), idesc, k != 0);
-          tc_commit(&empty[s]);
-          tc_commit(&acc_full[acc]);
+            for (int k = 0; k < kGroup / 32; ++k)  // 32 bytes along the swizzle atom
+              mma_e4m3(d, da0 + at + (uint64_t)(2 * k), db0 + at + (uint64_t)(2 * k), idesc, k != 0);
+            tc_commit(&empty[s]);
+            tc_commit(&acc_full[acc]);
+          }
+          __syncwarp();
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
@@ -229,176 +269,235 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (a.csize > 1) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
     // ------------------------------------------------------------ epilogue
     constexpr int kHalf = BN / 2;                      // columns of this warp
     constexpr int kCh = kHalf < 32 ? kHalf : 32;       // columns per TMEM load
     constexpr int kNCh = kHalf / kCh;
-    constexpr int kWs = WIDE ? (BN == 192 ? 3 : 1) : 1;  // weight scales of the warp's columns: 96 may straddle a block
-    const int q = warp & 3, half = (warp - 2) / 4;
+    constexpr int kTwo = kNCh > 1 ? 2 : 1;             // TMEM loads in flight
+    constexpr int kWs = WIDE && BN == 192 ? 3 : 1;     // weight scales of the warp's columns: 96 may straddle a block
+    constexpr int kAhead = 2;                          // groups whose scales are read at a time
+    const int q = warp & 3, half = (warp - kEpiWarp0) / 4;
     const int l = 32 * q + lane;                       // this thread's TMEM lane
     const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * kHalf);
     int acc = 0;
     uint32_t aph = 0;
-    for (int t = first; t < a.tiles; t += step) {
-      const int r0 = (t % a.lane_tiles) * kLanes, c0 = (t / a.lane_tiles) * BN + half * kHalf;
-      // this thread's share of a group's scales: its token's (wide: the lane's;
-      // tall: column c0 + lane's) and the weight blocks'
-      const int mtok = WIDE ? r0 + l : c0 + lane;
-      const bool has_tok = WIDE ? mtok < a.M : (lane < kHalf && mtok < a.M);
-      auto load_x = [&](int g) { return has_tok && g < g1 ? __ldg(a.xs + (size_t)g * a.M + mtok) : 0.f; };
-      auto load_w = [&](int g, int j) {
-        const int n = WIDE ? c0 + 32 * j : r0;
-        return g < g1 && n < a.N ? __ldg(a.ws + (size_t)(n >> 7) * a.groups + g) : 0.f;
-      };
-      float x0 = load_x(g0), x1 = load_x(g0 + 1);
-      float w0[kWs], w1[kWs];
+    // A thread's share of a group's scales: its token's (wide: the lane's; tall:
+    // column lane's) and the weight blocks'.  kAhead groups are read while the
+    // kAhead before are used, the next tile's first ones before this tile is
+    // stored.  Rows and groups outside are held to the last one (their products
+    // are not stored or not formed), so that the loads need no predicate.
+    float xs[kAhead], ws[kAhead][kWs];
+    const float* xp;
+    const float* wp[kWs];
+    auto seek = [&](const TileWalk& w) {
+      const int m = WIDE ? w.lt * kLanes + l : w.ct * BN + half * kHalf + (lane < kHalf ? lane : 0);
+      xp = a.xs + min(m, a.M - 1);
 #pragma unroll
       for (int j = 0; j < kWs; ++j) {
-        w0[j] = load_w(g0, j);
-        w1[j] = load_w(g0 + 1, j);
+        const int n = WIDE ? w.ct * BN + half * kHalf + 32 * j : w.lt * kLanes;
+        wp[j] = a.ws + (size_t)(min(n, a.N - 1) >> 7) * a.groups;
       }
+    };
+    auto load_scales = [&](float* x, float (*w)[kWs], int g) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int at = min(g + u, g1 - 1);
+        x[u] = __ldg(xp + (size_t)at * a.M);
+#pragma unroll
+        for (int j = 0; j < kWs; ++j) w[u][j] = __ldg(wp[j] + at);
+      }
+    };
+    TileWalk w(first, step, a.lane_tiles);
+    if (w.t < a.tiles) {
+      seek(w);
+      load_scales(xs, ws, g0);
+    }
+    while (w.t < a.tiles) {
+      const int r0 = w.lt * kLanes, c0 = w.ct * BN + half * kHalf;
       float2 sum[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) sum[i] = make_float2(0.f, 0.f);
-      for (int g = g0; g < g1; ++g) {
-        const float x2 = load_x(g + 2);
-        float w2[kWs];
+      for (int gg = g0; gg < g1; gg += kAhead) {
+        float xn[kAhead], wn[kAhead][kWs];
+        load_scales(xn, wn, gg + kAhead);
 #pragma unroll
-        for (int j = 0; j < kWs; ++j) w2[j] = load_w(g + 2, j);
-        if (lane == 0 && !tc_wait(&acc_full[acc], aph)) atomicOr(a.err, kErrTimeout);
-        __syncwarp();
-        tc_fence_after();
+        for (int ahead = 0; ahead < kAhead; ++ahead) {
+          if (gg + ahead >= g1) break;
+          if (!tc_wait_asleep(&acc_full[acc], aph) && lane == 0) atomicOr(a.err, kErrTimeout);
+          tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < kNCh; ++c) {
-          float v[kCh];
-          tmem_ld<kCh>(tbase + (uint32_t)(acc * BN + c * kCh), v);
-          if (c == kNCh - 1) {  // the accumulator is read: the MMA may fill it again
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[acc]);
-          }
-          if constexpr (WIDE) {
-            const float f = x0 * w0[kWs > 1 ? c : 0];
+          for (int c = 0; c < kNCh; c += kTwo) {
+            uint32_t v[kTwo][kCh];
 #pragma unroll
-            for (int i = 0; i < kCh / 2; ++i)
-              sum[c * kCh / 2 + i] =
-                  __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f), sum[c * kCh / 2 + i]);
-          } else {
-            const float f = x0 * w0[0];
+            for (int u = 0; u < kTwo; ++u)
+              if (c + u < kNCh) tmem_ld<kCh>(tbase + (uint32_t)(acc * BN + (c + u) * kCh), v[u]);
+            tmem_wait();
+            if (c + kTwo >= kNCh) {  // the accumulator is read: the MMA may fill it again
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&acc_empty[acc]);
+            }
 #pragma unroll
-            for (int i = 0; i < kCh / 2; ++i) {
-              const float2 s2 = make_float2(__shfl_sync(0xffffffffu, f, c * kCh + 2 * i),
-                                            __shfl_sync(0xffffffffu, f, c * kCh + 2 * i + 1));
-              sum[c * kCh / 2 + i] = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), s2, sum[c * kCh / 2 + i]);
+            for (int u = 0; u < kTwo; ++u) {
+              if (c + u >= kNCh) continue;
+              const float f = xs[ahead] * ws[ahead][kWs > 1 ? c + u : 0];
+#pragma unroll
+              for (int i = 0; i < kCh / 2; ++i) {
+                const int at = (c + u) * kCh / 2 + i;
+                const float2 s2 = WIDE ? make_float2(f, f)
+                                       : make_float2(__shfl_sync(0xffffffffu, f, (c + u) * kCh + 2 * i),
+                                                     __shfl_sync(0xffffffffu, f, (c + u) * kCh + 2 * i + 1));
+                sum[at] = __ffma2_rn(make_float2(__uint_as_float(v[u][2 * i]), __uint_as_float(v[u][2 * i + 1])),
+                                     s2, sum[at]);
+              }
             }
           }
+          if (++acc == SM::kAcc) {
+            acc = 0;
+            aph ^= 1u;
+          }
         }
-        x0 = x1;
-        x1 = x2;
 #pragma unroll
-        for (int j = 0; j < kWs; ++j) {
-          w0[j] = w1[j];
-          w1[j] = w2[j];
+        for (int u = 0; u < kAhead; ++u) {
+          xs[u] = xn[u];
+#pragma unroll
+          for (int j = 0; j < kWs; ++j) ws[u][j] = wn[u][j];
         }
-        if (++acc == SM::kAcc) {
-          acc = 0;
-          aph ^= 1u;
-        }
+      }
+      w.next();
+      if (w.t < a.tiles) {
+        seek(w);
+        load_scales(xs, ws, g0);
       }
       if (a.csize > 1) {
         // every load of the ring has been consumed by a completed MMA
-        float* part = reinterpret_cast<float*>(smem) + (size_t)(half * kHalf) * SM::kPartStride + l;
+        float* part = reinterpret_cast<float*>(smem);
 #pragma unroll
         for (int i = 0; i < kHalf / 2; ++i) {
-          part[(2 * i) * SM::kPartStride] = sum[i].x;
-          part[(2 * i + 1) * SM::kPartStride] = sum[i].y;
+          if constexpr (WIDE) {
+            if (i % 2 == 0)
+              *reinterpret_cast<float4*>(part + (size_t)l * SM::kPartStride + half * kHalf + 2 * i) =
+                  make_float4(sum[i].x, sum[i].y, sum[i + 1].x, sum[i + 1].y);
+          } else {
+            part[(half * kHalf + 2 * i) * SM::kPartStride + l] = sum[i].x;
+            part[(half * kHalf + 2 * i + 1) * SM::kPartStride + l] = sum[i].y;
+          }
         }
       } else if constexpr (WIDE) {
-        const int m = r0 + l;
-        if (m < a.M) {
-          if (a.vec && c0 + kHalf <= a.N) {
-            if (a.out_f32) {
-              float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + (size_t)m * a.N + c0);
-              const float4* b = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.bias) + c0);
+        if (a.tma_out) {
+          // 32 tokens x 128 bytes at a time go to shared memory (16-byte chunk j
+          // of row r at j ^ (r % 8), the tensor map's swizzle: no bank conflicts)
+          // and leave by TMA, which also drops what lies outside the output.
+          // (Stored by the threads, a row per lane, a tile's 64 KB took 13000
+          // cycles against its 12 groups' 6100.)
+          constexpr int kPer = 128 / (int)sizeof(T);     // columns of a part
+          constexpr int kV = Storage<T>::kVec;
+          uint8_t* turn = smem + SM::kTurn + (size_t)(warp - kEpiWarp0) * 4096;
 #pragma unroll
-              for (int i = 0; i < kHalf / 4; ++i) {
-                float4 y = make_float4(sum[2 * i].x, sum[2 * i].y, sum[2 * i + 1].x, sum[2 * i + 1].y);
-                if (a.bias) {
-                  const float4 bb = __ldg(b + i);
-                  y = make_float4(y.x + bb.x, y.y + bb.y, y.z + bb.z, y.w + bb.w);
-                }
-                o[i] = y;
+          for (int p = 0; p < (kHalf + kPer - 1) / kPer; ++p) {
+            if (lane == 0) bulk_wait_read();  // the part before has left
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (p * kPer + j * kV >= kHalf) continue;
+              float y[kV];
+#pragma unroll
+              for (int e = 0; e < kV / 2; ++e) {
+                y[2 * e] = sum[(p * kPer + j * kV) / 2 + e].x;
+                y[2 * e + 1] = sum[(p * kPer + j * kV) / 2 + e].y;
+              }
+              if (a.bias) {
+                const int n = c0 + p * kPer + j * kV;
+                float b[kV];
+                unpack16<T>(n < a.N ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.bias) + n))
+                                    : make_uint4(0u, 0u, 0u, 0u),
+                            b);
+#pragma unroll
+                for (int e = 0; e < kV; ++e) y[e] += b[e];
+              }
+              *reinterpret_cast<uint4*>(turn + lane * 128 + ((j ^ (lane & 7)) << 4)) = pack16<T>(y);
+            }
+            fence_async_smem();
+            __syncwarp();
+            // (a half part, 96 bf16 columns' last, ends inside its 64-column box:
+            // its stale second half would land on the next warp's columns)
+            const bool whole = (p + 1) * kPer <= kHalf;
+            if (whole) {
+              if (lane == 0 && c0 + p * kPer < a.N && r0 + 32 * q < a.M) {
+                tma_store_2d(&to, c0 + p * kPer, r0 + 32 * q, turn);
+                bulk_commit();
               }
             } else {
-              uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(a.out) + (size_t)m * a.N + c0);
-              const uint4* b = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(a.bias) + c0);
-#pragma unroll
-              for (int i = 0; i < kHalf / 8; ++i) {
-                float y[8];
+              const int r = lane, m = r0 + 32 * q + r;
+              if (m < a.M)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  y[2 * j] = sum[4 * i + j].x;
-                  y[2 * j + 1] = sum[4 * i + j].y;
+                  const int n = c0 + p * kPer + j * kV;
+                  if (n < a.N)
+                    *reinterpret_cast<uint4*>(reinterpret_cast<T*>(a.out) + (size_t)m * a.N + n) =
+                        *reinterpret_cast<const uint4*>(turn + r * 128 + ((j ^ (r & 7)) << 4));
                 }
-                if (a.bias) {
-                  float bb[8];
-                  unpack16<bf16>(__ldg(b + i), bb);
-#pragma unroll
-                  for (int j = 0; j < 8; ++j) y[j] += bb[j];
-                }
-                o[i] = pack16<bf16>(y);
-              }
             }
-          } else {
+          }
+        } else if (const int m = r0 + l; m < a.M) {
 #pragma unroll
-            for (int i = 0; i < kHalf / 2; ++i) {
-              if (c0 + 2 * i < a.N) store_out(a, m, c0 + 2 * i, sum[i].x);
-              if (c0 + 2 * i + 1 < a.N) store_out(a, m, c0 + 2 * i + 1, sum[i].y);
-            }
+          for (int i = 0; i < kHalf / 2; ++i) {
+            if (c0 + 2 * i < a.N) store_out<T>(a, m, c0 + 2 * i, sum[i].x);
+            if (c0 + 2 * i + 1 < a.N) store_out<T>(a, m, c0 + 2 * i + 1, sum[i].y);
           }
         }
       } else {
-        const int n = r0 + l;
+        const int n = r0 + l, left = a.M - c0;
         if (n < a.N) {
+          const float b = a.bias ? to_f(reinterpret_cast<const T*>(a.bias)[n]) : 0.f;
+          T* o = reinterpret_cast<T*>(a.out) + (size_t)c0 * a.N + n;
 #pragma unroll
           for (int i = 0; i < kHalf / 2; ++i) {
-            if (c0 + 2 * i < a.M) store_out(a, c0 + 2 * i, n, sum[i].x);
-            if (c0 + 2 * i + 1 < a.M) store_out(a, c0 + 2 * i + 1, n, sum[i].y);
+            if (2 * i < left) o[0] = from_f<T>(sum[i].x + b);
+            if (2 * i + 1 < left) o[a.N] = from_f<T>(sum[i].y + b);
+            o += 2 * (size_t)a.N;
           }
         }
       }
     }
-  }
-
-  if (a.csize > 1) {
-    namespace cg = cooperative_groups;
-    cg::cluster_group cl = cg::this_cluster();
-    __syncwarp();
-    cl.sync();  // the partial tiles are written
-    const int t = first;
-    const int r0 = (t % a.lane_tiles) * kLanes, c0 = (t / a.lane_tiles) * BN;
-    const float* part = reinterpret_cast<const float*>(smem);
-    const float* peer[kClusterMax];
+    if (WIDE && lane == 0) bulk_wait_all();
+    if (a.csize > 1) {
+      namespace cg = cooperative_groups;
+      cg::cluster_group cl = cg::this_cluster();
+      __syncwarp();
+      cluster_sync();  // the partial tiles are written
+      const int t = first;
+      const int r0 = (t % a.lane_tiles) * kLanes, c0 = (t / a.lane_tiles) * BN;
+      const float* part = reinterpret_cast<const float*>(smem);
+      // this CTA adds the tokens o % csize == rank, four features per thread
+      constexpr int kFeat = WIDE ? BN : kLanes, kTok = WIDE ? kLanes : BN;
+      for (int i = threadIdx.x - kEpiWarp0 * 32; i < (kTok - rank + a.csize - 1) / a.csize * (kFeat / 4); i += kEpiWarps * 32) {
+        const int f = i % (kFeat / 4) * 4, o = i / (kFeat / 4) * a.csize + rank;
+        const int m = (WIDE ? r0 : c0) + o, n = (WIDE ? c0 : r0) + f;
+        if (m >= a.M || n >= a.N) continue;
+        float4 v[kClusterMax];
 #pragma unroll
-    for (int r = 0; r < kClusterMax; ++r)
-      peer[r] = r < a.csize ? cl.map_shared_rank(part, r) : part;
-    // wide: this CTA takes the token rows l % csize == rank, threads along the
-    // features; tall: the token columns c % csize == rank, threads along the
-    // features again (the lanes): either way a warp stores a row's neighbours
-    constexpr int kAlong = WIDE ? BN : kLanes, kOther = WIDE ? kLanes : BN;
-    for (int i = threadIdx.x; i < (kOther - rank + a.csize - 1) / a.csize * kAlong; i += kThreads) {
-      const int f = i % kAlong, o = i / kAlong * a.csize + rank;
-      const int m = (WIDE ? r0 : c0) + o, n = (WIDE ? c0 : r0) + f;
-      if (m >= a.M || n >= a.N) continue;
-      const size_t at = WIDE ? (size_t)f * SM::kPartStride + o : (size_t)o * SM::kPartStride + f;
-      float y = 0.f;
+        for (int r = 0; r < kClusterMax; ++r)
+          if (r < a.csize)
+            v[r] = *reinterpret_cast<const float4*>(cl.map_shared_rank(part, r) + (size_t)o * SM::kPartStride + f);
+        float4 y = v[0];
 #pragma unroll
-      for (int r = 0; r < kClusterMax; ++r)
-        if (r < a.csize) y += peer[r][at];
-      store_out(a, m, n, y);
+        for (int r = 1; r < kClusterMax; ++r)
+          if (r < a.csize) y = make_float4(y.x + v[r].x, y.y + v[r].y, y.z + v[r].z, y.w + v[r].w);
+        store_out<T>(a, m, n, y.x);
+        if (n + 1 < a.N) store_out<T>(a, m, n + 1, y.y);
+        if (n + 2 < a.N) store_out<T>(a, m, n + 2, y.z);
+        if (n + 3 < a.N) store_out<T>(a, m, n + 3, y.w);
+      }
+      cluster_sync();  // no CTA leaves while another reads its tile
     }
-    cl.sync();  // no CTA leaves while another reads its tile
   }
   tc_fence_before();
   __syncthreads();
@@ -409,11 +508,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool WIDE, int BN, int STAGES>
+template <typename T, bool WIDE, int BN, int STAGES>
 q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t st) {
-  using SM = Q8Smem<BN, STAGES>;
-  auto* kernel = q8_linear_kernel<WIDE, BN, STAGES>;
+  using SM = Q8Smem<WIDE, BN, STAGES>;
+  auto* kernel = q8_linear_kernel<T, WIDE, BN, STAGES>;
   Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
+  // the register split draws on what the kernel is launched with: fewer would
+  // leave setmaxnreg.inc waiting
+  cudaFuncAttributes fa;
+  Q2_CUDA_TRY(cudaFuncGetAttributes(&fa, kernel));
+  if (fa.numRegs * kThreads < kRegsLow * kEpiWarp0 * 32 + kRegsHigh * kEpiWarps * 32) {
+    set_error("linear_q8: the kernel was built with too few registers for its split");
+    return Q2_ERR_CUDA;
+  }
   a.lane_tiles = ((WIDE ? a.M : a.N) + kLanes - 1) / kLanes;
   const long long tiles = (long long)a.lane_tiles * (((WIDE ? a.N : a.M) + BN - 1) / BN);
   if (tiles >= (1ll << 30)) {
@@ -431,6 +538,17 @@ q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t
   CUtensorMap tx, tw;
   Q2_TRY(make_tmap_2d_u8(&tx, xq, (uint64_t)a.M, (uint64_t)K, (uint64_t)K, WIDE ? kLanes : BN, kGroup, 128));
   Q2_TRY(make_tmap_2d_u8(&tw, wq, (uint64_t)a.N, (uint64_t)K, (uint64_t)K, WIDE ? BN : kLanes, kGroup, 128));
+  // the output by TMA where its rows start on 16 bytes
+  CUtensorMap to = {};
+  a.tma_out = WIDE && a.csize == 1 &&
+              ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.bias) | (a.N * sizeof(T))) & 15) == 0;
+  if (a.tma_out) {
+    const uint64_t pitch = (uint64_t)a.N * sizeof(T);
+    if (sizeof(T) == 2)
+      Q2_TRY(make_tmap_2d_bf16(&to, a.out, (uint64_t)a.M, (uint64_t)a.N, pitch, 32, 64, 128));
+    else
+      Q2_TRY(make_tmap_2d_f32(&to, a.out, (uint64_t)a.M, (uint64_t)a.N, pitch, 32, 32, 128));
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.csize > 1 ? tiles * a.csize : tiles < sms ? tiles : sms));
   cfg.blockDim = dim3(kThreads);
@@ -445,8 +563,21 @@ q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  Q2_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, WIDE ? tx : tw, WIDE ? tw : tx, a));
+  Q2_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, WIDE ? tx : tw, WIDE ? tw : tx, to, a));
   return Q2_OK;
+}
+
+template <typename T>
+q2_status linear_t(const void* xq, const void* wq, int K, const Q8Lin& a, cudaStream_t st) {
+  if (a.M <= 16) return launch_q8<T, false, 16, 11>(xq, wq, K, a, st);
+  if (a.M <= 32) return launch_q8<T, false, 32, 10>(xq, wq, K, a, st);
+  if (a.M <= 64) return launch_q8<T, false, 64, 8>(xq, wq, K, a, st);
+  const int sms = num_sms();
+  const long long lt = (a.M + kLanes - 1) / kLanes;
+  auto cost = [&](int bn) { return (lt * ((a.N + bn - 1) / bn) + sms - 1) / sms * bn; };
+  if (lt * ((a.N + 255) / 256) < sms) return launch_q8<T, true, 128, 6>(xq, wq, K, a, st);
+  if (10 * cost(192) <= 9 * cost(256)) return launch_q8<T, true, 192, 4>(xq, wq, K, a, st);
+  return launch_q8<T, true, 256, 4>(xq, wq, K, a, st);
 }
 
 }  // namespace
@@ -468,7 +599,6 @@ extern "C" q2_status q2_linear_q8(void* out, const void* xq, const float* xs, co
                "linear_q8: the codes must be 16-byte aligned");
   int* flag = op_error_flag();
   Q2_CHECK_ARG(flag, Q2_ERR_CUDA, "cannot resolve the device error flag");
-  const size_t es = dtype == Q2_BF16 ? 2 : 4;
   Q8Lin a = {};
   a.xs = xs;
   a.ws = ws;
@@ -477,17 +607,7 @@ extern "C" q2_status q2_linear_q8(void* out, const void* xq, const float* xs, co
   a.M = (int)M;
   a.N = (int)N;
   a.groups = (int)((K + kGroup - 1) / kGroup);
-  a.out_f32 = dtype == Q2_F32;
-  a.vec = ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(bias) | (N * es)) & 15) == 0;
   a.err = flag;
   cudaStream_t st = as_stream(stream);
-  if (M <= 16) return launch_q8<false, 16, 11>(xq, wq, (int)K, a, st);
-  if (M <= 32) return launch_q8<false, 32, 10>(xq, wq, (int)K, a, st);
-  if (M <= 64) return launch_q8<false, 64, 8>(xq, wq, (int)K, a, st);
-  const int sms = num_sms();
-  const long long lt = (a.M + kLanes - 1) / kLanes;
-  auto cost = [&](int bn) { return (lt * ((a.N + bn - 1) / bn) + sms - 1) / sms * bn; };
-  if (lt * ((a.N + 255) / 256) < sms) return launch_q8<true, 128, 6>(xq, wq, (int)K, a, st);
-  if (10 * cost(192) <= 9 * cost(256)) return launch_q8<true, 192, 5>(xq, wq, (int)K, a, st);
-  return launch_q8<true, 256, 4>(xq, wq, (int)K, a, st);
+  return dtype == Q2_BF16 ? linear_t<bf16>(xq, wq, (int)K, a, st) : linear_t<float>(xq, wq, (int)K, a, st);
 }

@@ -26,6 +26,26 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// The same for warps that wait in every step of a pipeline: the try itself may
+// sleep (up to 1 ms) instead of coming back at once, so that waiting warps
+// leave the issue slots to the others.
+__device__ __forceinline__ bool tc_wait_asleep(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    const uint64_t now = tc_gtimer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kTcDeadlineNs) return false;
+  }
+}
+
 // Shared-memory matrix descriptor of a K-major, 128-byte-swizzled tile whose
 // 8-row groups are 1024 bytes apart (what a TMA box of 64 bf16 columns with
 // 128-byte swizzle lays down): start address, leading offset 16 B (unused
@@ -41,6 +61,13 @@ __device__ __forceinline__ void tc_fence_before() {
 }
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// One lane of a converged warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 // Arrive on `bar` once every MMA issued so far by this thread has completed.

@@ -69,4 +69,10 @@ q2_status make_tmap_2d_u8(CUtensorMap* out, const void* base, uint64_t rows, uin
                       swizzle_bytes);
 }
 
+q2_status make_tmap_2d_f32(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
+                           uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols, int swizzle_bytes) {
+  return make_tmap_2d(out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, rows, cols, pitch_bytes, box_rows, box_cols,
+                      swizzle_bytes);
+}
+
 }  // namespace q2
