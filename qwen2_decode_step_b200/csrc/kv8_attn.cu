@@ -1,11 +1,38 @@
 // kv8_attn.cu -- attention over the 8-bit KV cache.
 //
-// One CTA per (query head, query row, sequence): online softmax in fp32 over
-// tiles of 128 keys, one key per thread for the scores, one dimension per
-// thread for the output.
+// Split kernel (any head dim, fp32 or bf16, one to many query rows).  The
+// query rows of a kv head (ntok rows x nh / nkv heads) go on the M side of
+// mma.sync m16n8k16 (16 rows an m-tile, up to four m-tiles a work item), keys
+// on N for the scores, head dims on N for the output.  A work item is (sequence,
+// m-tiles, kv head); its unit of work is one block of 64 keys -- one scale of K
+// and one of V.  All items' blocks, in order, are dealt to a grid of resident
+// CTAs in equal runs (lengths are read on the device), so ragged batches and a
+// single long sequence load every SM alike; an item cut by a run's end leaves
+// partial results that a second kernel joins in order (the same result every
+// time).
+//
+// Bound by HBM (a byte per cached element): 64-key K and V tiles arrive by TMA
+// in a ring (swizzled to the head's row length) fed by one warp; four warps
+// consume, a block at a time each (or, with several m-tiles, one m-tile each of
+// the same block).  e4m3 values are exact in fp16 and Blackwell converts two
+// per instruction, so the products run in fp16 with fp32 accumulation:
+//   scores  a lane's 32 contiguous bytes of a key row (16-byte loads, no bank
+//           conflicts under the swizzle) feed eight MMAs: the order of the dims
+//           inside a dot product is free, the query's fragments take the same;
+//   output  ldmatrix.trans on byte pairs gives a lane two keys x two dims; one
+//           byte permute splits them into the even and the odd dim's operand.
+// The query rows are scaled by a power of two into fp16's range (exact for
+// bf16; fp32 queries are split into a high and a low fp16 part, two MMAs, and
+// so are their probabilities).  Softmax in fp32, online, with p = 2^(s - m + 14):
+// the common factor cancels and keeps probabilities down to 2^-28 of the
+// largest at fp16's full 11 bits.  The scale of K multiplies the scores; the
+// output is accumulated in units of the current block's V scale and moved to
+// the next block's where that differs (a power of two: exact).
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "kv8.h"
+#include "tcgen05.cuh"
+#include "tma.h"
 
 namespace q2 {
 
@@ -13,93 +40,731 @@ namespace {
 
 constexpr int kBlk = Q2_KV8_BLOCK;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kWarps = 4;                       // consumers
+constexpr int kThreads = (kWarps + 1) * 32;     // and the producer
+constexpr int kRing = 4;                        // a multiple of kWarps: a slot always meets the same warps
+constexpr int kCtasMax = 512;
+constexpr float kPBias = 14.f;                  // p <= 2^14 in fp16
 
 struct Kv8Attn {
   const void* q;
   long long q_seq_stride, q_tok_stride;
-  const uint8_t* kc;
-  const uint8_t* vc;
   const float* ks;
   const float* vs;
   const int32_t* lens;  // [batch] keys of each sequence; null: fixed_len
   int fixed_len;
   int batch, ntok, nh, nkv, max_seq, nblk;
+  int nm;       // m-tiles of an item: 1, 2 or 4
+  int mgroups;  // items of a (sequence, kv head)
   float scale;
-  void* out;  // [batch][ntok][nh][hd]
+  void* out;    // [batch][ntok][nh][hd]
+  float* part;  // [2 * CTAs][16 nm][hd + 2]: rows of partial items, then m and l of each row
+  int ctas;     // of the split kernel
   int* err;
 };
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a) {
-  __shared__ float qs[HD], p[128], red[4];
-  const int h = blockIdx.x, t = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int g = h / (a.nh / a.nkv);
-  int len = a.lens ? a.lens[b] : a.fixed_len;
-  if (len > a.max_seq) {
-    if (tid == 0) atomicOr(a.err, kErrCapacity);
-    len = 0;
-  }
-  const int n = max(0, len - a.ntok + 1 + t);  // keys that this row sees
-  const T* q = reinterpret_cast<const T*>(a.q) + (long long)b * a.q_seq_stride + (long long)t * a.q_tok_stride +
-               (long long)h * HD;
-  if (tid < HD) qs[tid] = to_f(q[tid]);
-  const size_t head = (size_t)b * a.nkv + g;
-  const uint8_t* kc = a.kc + head * a.max_seq * HD;
-  const uint8_t* vc = a.vc + head * a.max_seq * HD;
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 128) {
-    __syncthreads();
-    float s = -INFINITY;
-    if (k0 + tid < n) {
-      s = 0.f;
-      const uint32_t* row = reinterpret_cast<const uint32_t*>(kc + (size_t)(k0 + tid) * HD);
-      for (int d = 0; d < HD / 4; ++d) {
-        float f[4];
-        e4m3x4_to_f(row[d], f);
-        for (int j = 0; j < 4; ++j) s = fmaf(f[j], qs[4 * d + j], s);
-      }
-      s *= a.scale * kLog2e * a.ks[head * a.nblk + (k0 + tid) / kBlk];
-    }
-    float w = warp_max(s);
-    if ((tid & 31) == 0) red[tid >> 5] = w;
-    __syncthreads();
-    const float mn = fmaxf(fmaxf(m, fmaxf(red[0], red[1])), fmaxf(red[2], red[3]));
-    const float ms = mn == -INFINITY ? 0.f : mn;
-    const float e = exp2f(s - ms);
-    p[tid] = e;
-    w = warp_sum(e);
-    __syncthreads();
-    if ((tid & 31) == 0) red[tid >> 5] = w;
-    __syncthreads();
-    const float alpha = exp2f(m - ms);
-    l = l * alpha + ((red[0] + red[1]) + (red[2] + red[3]));
-    o *= alpha;
-    m = mn;
-    if (tid < HD)
-      for (int j = 0; j < min(128, n - k0); ++j) {
-        float f[4];
-        e4m3x4_to_f(vc[(size_t)(k0 + j) * HD + tid], f);
-        o = fmaf(p[j], f[0] * a.vs[head * a.nblk + (k0 + j) / kBlk], o);
-      }
-  }
-  if (tid < HD)
-    reinterpret_cast<T*>(a.out)[(((size_t)b * a.ntok + t) * a.nh + h) * HD + tid] =
-        from_f<T>(l == 0.f ? 0.f : o / l);
+// --------------------------------------------------------------- work division
+
+__device__ __forceinline__ int seq_len(const Kv8Attn& a, int b) {
+  const int n = a.lens ? a.lens[b] : a.fixed_len;
+  return n > a.max_seq || n < 0 ? 0 : n;
+}
+// Query token of row r of a kv head's rows.
+__device__ __forceinline__ int row_tok(const Kv8Attn& a, int r) { return r / (a.nh / a.nkv); }
+// Blocks that an item's rows see (the last row sees the most).
+__device__ __forceinline__ int item_blocks(const Kv8Attn& a, int len, int mg) {
+  const int rows = a.ntok * (a.nh / a.nkv);
+  const int last = min(rows, (mg + 1) * a.nm * 16) - 1;
+  const int keys = max(0, len - a.ntok + 1 + row_tok(a, last));
+  return (keys + kBlk - 1) / kBlk;
 }
 
-template <typename T>
-q2_status simple_t(const Kv8Attn& a, int hd, cudaStream_t st) {
-  const dim3 grid(a.nh, a.ntok, a.batch);
-  switch (hd) {
-    case 32: Q2_LAUNCH(kv8_attn_simple_kernel<T, 32>, grid, dim3(128), 0, st, false, a); break;
-    case 64: Q2_LAUNCH(kv8_attn_simple_kernel<T, 64>, grid, dim3(128), 0, st, false, a); break;
-    default: Q2_LAUNCH(kv8_attn_simple_kernel<T, 128>, grid, dim3(128), 0, st, false, a); break;
+// Entries e = (sequence, m-group), e = b * mgroups + mg, hold nkv items of
+// item_blocks() units each.
+__device__ __forceinline__ int entry_units(const Kv8Attn& a, int e) {
+  const int b = e / a.mgroups;
+  return a.nkv * item_blocks(a, seq_len(a, b), e - b * a.mgroups);
+}
+// Every thread of the CTA (n, a multiple of 32) takes entries [*e0, *e1) and gets
+// the units before them; returns all entries' units.
+__device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int n, int* s_warp, int* mine_before,
+                                            int* e0, int* e1) {
+  const int entries = a.batch * a.mgroups, per = (entries + n - 1) / n;
+  *e0 = min(entries, tid * per);
+  *e1 = min(entries, *e0 + per);
+  int sum = 0;
+  for (int e = *e0; e < *e1; ++e) sum += entry_units(a, e);
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
+    if ((tid & 31) >= o) inc += v;
   }
+  if ((tid & 31) == 31) s_warp[tid >> 5] = inc;
+  __syncthreads();
+  int base = 0, total = 0;
+  for (int w = 0; w < n / 32; ++w) {
+    if (w < (tid >> 5)) base += s_warp[w];
+    total += s_warp[w];
+  }
+  *mine_before = base + inc - sum;
+  return total;
+}
+// Units per CTA: equal runs, at least one block per key-splitting warp.
+__device__ __forceinline__ int run_units(const Kv8Attn& a, int total) {
+  return max((total + a.ctas - 1) / a.ctas, kWarps / a.nm);
+}
+
+// ------------------------------------------------------------------- fragments
+
+// Byte offset of 16-byte chunk c of row r in a tile of rows of HD bytes laid
+// down by TMA with an HD-byte swizzle.
+template <int HD>
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  constexpr int kShift = HD == 128 ? 0 : HD == 64 ? 1 : 2, kMask = HD / 16 - 1;
+  return (uint32_t)(r * HD + ((c ^ ((r >> kShift) & kMask)) << 4));
+}
+
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* x, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+template <int BYTES>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+  float2 f;
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.f32.f16 %0, a;\n cvt.f32.f16 %1, b;\n}\n"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(v));
+  return f;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Which of the four codes of a word are NaN, as 0xff bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t v) {
+  return __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+__device__ __forceinline__ void store_row4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+template <typename T, int HD>
+struct SplitSmem {
+  static constexpr size_t kTile = (size_t)kBlk * HD;
+  static constexpr size_t kSlot = 2 * kTile;
+  // a segment's rows of the four warps, rows 16 floats longer against conflicts
+  static constexpr int kRowF = HD + 16;
+  static constexpr size_t kO = kRing * kSlot;
+  static constexpr size_t kML = kO + (size_t)kWarps * 16 * kRowF * 4;
+  static constexpr size_t kBars = kML + (size_t)kWarps * 16 * 2 * 4;
+  static constexpr size_t kInts = kBars + 2 * kRing * 8;
+  static constexpr size_t kTotal = kInts + 16 * 4 + 1024;
+};
+
+// Walks a CTA's units: item by item, block by block.
+struct UnitWalk {
+  int e, b, mg, g, len, nb, blk;  // entry, its sequence and m-group, kv head, keys, blocks of an item, block
+  __device__ __forceinline__ void entry_of(const Kv8Attn& a) {
+    b = e / a.mgroups;
+    mg = e - b * a.mgroups;
+    len = seq_len(a, b);
+    nb = item_blocks(a, len, mg);
+  }
+  __device__ __forceinline__ void seek(const Kv8Attn& a, int entry, int rem) {
+    e = entry;
+    entry_of(a);
+    g = rem / nb;
+    blk = rem - g * nb;
+  }
+  // to the first block of the next item (there is one)
+  __device__ __forceinline__ void next_item(const Kv8Attn& a) {
+    blk = 0;
+    if (++g == a.nkv) {
+      g = 0;
+      do {
+        ++e;
+        entry_of(a);
+      } while (nb == 0);
+    }
+  }
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+    kv8_split_kernel(const Kv8Attn a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using SM = SplitSmem<T, HD>;
+  constexpr bool kWide = sizeof(T) == 4;  // fp32: two fp16 parts of q and of p
+  constexpr int kTerms = kWide ? 2 : 1;
+  constexpr int kKeys = kWide ? 32 : 64;  // keys per softmax step (fp32's extra parts need the registers)
+  constexpr int kNt = kKeys / 8, kC = HD / 16;
+  extern __shared__ __align__(1024) uint8_t kv8_smem_raw[];
+  uint8_t* smem = kv8_smem_raw + ((1024u - (smem_u32(kv8_smem_raw) & 1023u)) & 1023u);
+  float* Ow = reinterpret_cast<float*>(smem + SM::kO);
+  float* MLw = reinterpret_cast<float*>(smem + SM::kML);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);
+  uint64_t* empty = full + kRing;
+  int* s_int = reinterpret_cast<int*>(smem + SM::kInts);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], a.nm);
+    }
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  pdl_wait();
+
+  // this CTA's run of units
+  int before, e0, e1;
+  const int total = scan_entries(a, tid, kThreads, s_int + 4, &before, &e0, &e1);
+  const int run = run_units(a, total);
+  const int u0 = (int)min((long long)blockIdx.x * run, (long long)total), u1 = min(total, u0 + run);
+  if (u0 < u1)
+    for (int e = e0; e < e1; ++e) {
+      const int n = entry_units(a, e);
+      if (before <= u0 && u0 < before + n) {
+        s_int[0] = e;
+        s_int[1] = u0 - before;
+      }
+      before += n;
+    }
+  if (blockIdx.x == 0 && a.lens)
+    for (int b = tid; b < a.batch; b += kThreads)
+      if (a.lens[b] > a.max_seq) atomicOr(a.err, kErrCapacity);
+  __syncthreads();
+  if (u0 >= u1) return;
+  UnitWalk w;
+  w.seek(a, s_int[0], s_int[1]);
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int u = u0; u < u1;) {
+        const int row = (w.b * a.nkv + w.g) * a.max_seq;
+        for (; w.blk < w.nb && u < u1; ++w.blk, ++u) {
+          uint8_t* st = smem + s * SM::kSlot;
+          if (!tc_wait_asleep(&empty[s], ph ^ 1u)) atomicOr(a.err, kErrTimeout);
+          mbar_arrive_expect_tx(&full[s], (uint32_t)SM::kSlot);
+          tma_load_2d(st, &kmap, 0, row + w.blk * kBlk, &full[s]);
+          tma_load_2d(st + SM::kTile, &vmap, 0, row + w.blk * kBlk, &full[s]);
+          if (++s == kRing) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (u < u1) w.next_item(a);
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int kw = kWarps / a.nm;            // warps that split the keys of an m-tile
+  const int mt = warp % a.nm, kg = warp / a.nm;
+  const int gq = lane >> 2, tq = lane & 3;
+  const int G = a.nh / a.nkv, rows = a.ntok * G;
+  const int mi = lane >> 3, mr = lane & 7;
+  const float sl2 = a.scale * kLog2e;
+  int i = 0;  // units of this CTA before the current item
+  for (int u = u0; u < u1;) {
+    const int n = min(w.nb - w.blk, u1 - u);       // units of this item here
+    const bool whole = n == w.nb;
+    const int m0 = (w.mg * a.nm + mt) * 16;        // the m-tile's first row
+    const bool two = m0 + 8 < rows;                // rows 8..15 exist
+    const size_t head = (size_t)w.b * a.nkv + w.g;
+    const float* ksp = a.ks + head * a.nblk;
+    const float* vsp = a.vs + head * a.nblk;
+
+    // query fragments: rows gq and gq + 8, the lane's HD / 4 contiguous dims
+    uint32_t qa[kTerms][HD / 16][4];
+    float sc[2];
+    int lim[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = m0 + gq + 8 * h;
+      float f[HD / 4];
+      lim[h] = 0;
+      if (r < rows) {
+        const int t = row_tok(a, r), hq = r - t * G;
+        lim[h] = w.len - a.ntok + 1 + t;
+        const T* src = reinterpret_cast<const T*>(a.q) + (long long)w.b * a.q_seq_stride +
+                       (long long)t * a.q_tok_stride + (long long)(w.g * G + hq) * HD + tq * (HD / 4);
+        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+          constexpr int kV = Storage<T>::kVec;
+#pragma unroll
+          for (int j = 0; j < HD / 4 / kV; ++j) unpack16<T>(__ldg(reinterpret_cast<const uint4*>(src) + j), f + j * kV);
+        } else {
+#pragma unroll
+          for (int j = 0; j < HD / 4; ++j) f[j] = to_f(src[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < HD / 4; ++j) f[j] = 0.f;
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < HD / 4; ++j) m = fmaxf(m, fabsf(f[j]));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      // 2^k brings the row's largest magnitude to [256, 512)
+      const int k = m > 0.f ? min(126, 127 + 8 - (int)(__float_as_uint(m) >> 23)) : 0;
+      const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+      sc[h] = sl2 * __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+      for (int j = 0; j < HD / 16; ++j) {
+        const float x0 = f[4 * j] * up, x1 = f[4 * j + 1] * up, x2 = f[4 * j + 2] * up, x3 = f[4 * j + 3] * up;
+        qa[0][j][h] = pack_f16x2(x0, x1);
+        qa[0][j][2 + h] = pack_f16x2(x2, x3);
+        if constexpr (kWide) {
+          const float2 y0 = unpack_f16x2(qa[0][j][h]), y1 = unpack_f16x2(qa[0][j][2 + h]);
+          qa[1][j][h] = pack_f16x2(x0 - y0.x, x1 - y0.y);
+          qa[1][j][2 + h] = pack_f16x2(x2 - y1.x, x3 - y1.y);
+        }
+      }
+    }
+    // keys below every row's limit need no mask
+    const int clear = w.len - a.ntok + 1 + row_tok(a, min(m0, rows - 1));
+
+    float o[kC][8];  // per chunk of 16 dims: even dims' tile, odd dims' tile
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[c][j] = 0.f;
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float unit = 0.f, unit_max = 0.f;
+
+    // this warp's units of the item: CTA unit x with x % kw == kg
+    int x = i + (kg - i % kw + kw) % kw;
+    float ks_n = 0.f, vs_n = 0.f;
+    if (x < i + n) {
+      ks_n = __ldg(ksp + w.blk + x - i);
+      vs_n = __ldg(vsp + w.blk + x - i);
+    }
+    for (; x < i + n; x += kw) {
+      const int slot = x % kRing, blk = w.blk + x - i;
+      const float ksc = ks_n, vsc = vs_n;
+      if (x + kw < i + n) {
+        ks_n = __ldg(ksp + blk + kw);
+        vs_n = __ldg(vsp + blk + kw);
+      }
+      if (!tc_wait_asleep(&full[slot], (uint32_t)((x / kRing) & 1)) && lane == 0) atomicOr(a.err, kErrTimeout);
+      if (m0 >= rows) {  // an m-tile without rows (three of four)
+        if (lane == 0) mbar_arrive(&empty[slot]);
+        continue;
+      }
+      const uint32_t kt = smem_u32(smem + slot * SM::kSlot), vt = kt + (uint32_t)SM::kTile;
+      // the unit of this block's V scale (never 2^60 below the largest so far:
+      // the output in units of it stays in range)
+      unit_max = fmaxf(unit_max, vsc);
+      const float unit_new = fmaxf(fmaxf(vsc, unit_max * 0x1p-60f), 0x1p-126f);
+      const float ratio = unit_new == unit ? 1.f : unit / unit_new;
+      const float pf = vsc == unit_new ? 1.f : vsc / unit_new;
+      unit = unit_new;
+#pragma unroll
+      for (int step = 0; step < kBlk / kKeys; ++step) {
+        const int key0 = blk * kBlk + step * kKeys;
+        const bool edge = key0 + kKeys > clear;
+        // ---- scores
+        float s[kNt][4];
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+          s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+          const int r = step * kKeys + nt * 8 + gq;
+          uint32_t kb[HD / 16];
+          if constexpr (HD == 128) {
+            lds_words<16>(kt + tile_off<HD>(r, 2 * tq), kb);
+            lds_words<16>(kt + tile_off<HD>(r, 2 * tq + 1), kb + 4);
+          } else if constexpr (HD == 64) {
+            lds_words<16>(kt + tile_off<HD>(r, tq), kb);
+          } else {
+            lds_words<8>(kt + tile_off<HD>(r, tq >> 1) + 8 * (tq & 1), kb);
+          }
+#pragma unroll
+          for (int j = 0; j < HD / 16; ++j) {
+            const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(kb[j] & 0xffffu));
+            const uint32_t b1 = e4m3x2_to_f16x2((uint16_t)(kb[j] >> 16));
+            mma_f16(s[nt], qa[0][j], b0, b1);
+            if constexpr (kWide) mma_f16(s[nt], qa[1][j], b0, b1);
+          }
+        }
+        // ---- softmax of rows gq (h = 0) and gq + 8 (h = 1)
+        uint32_t pa[kTerms][kNt / 2][4];
+        float alpha[2] = {1.f, 1.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h == 1 && !two) {
+#pragma unroll
+            for (int e = 0; e < kTerms; ++e)
+#pragma unroll
+              for (int kk = 0; kk < kNt / 2; ++kk) pa[e][kk][1] = pa[e][kk][3] = 0u;
+            continue;
+          }
+          const float f = sc[h] * ksc;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float v = s[nt][2 * h + j] * f;
+              if (edge && key0 + nt * 8 + 2 * tq + j >= lim[h]) v = -INFINITY;
+              s[nt][2 * h + j] = v;
+              mx = fmaxf(mx, v);
+            }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m_run[h], mx);
+          const float ms = mn == -INFINITY ? 0.f : mn;
+          alpha[h] = ex2(m_run[h] - ms);
+          m_run[h] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float p = ex2(s[nt][2 * h + j] - ms + kPBias);
+              s[nt][2 * h + j] = p;
+              sum += p;
+            }
+          l_run[h] = l_run[h] * alpha[h] + sum;
+          if (pf != 1.f) {
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) {
+              s[nt][2 * h] *= pf;
+              s[nt][2 * h + 1] *= pf;
+            }
+          }
+#pragma unroll
+          for (int kk = 0; kk < kNt / 2; ++kk)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              const float p0 = s[2 * kk + v][2 * h], p1 = s[2 * kk + v][2 * h + 1];
+              pa[0][kk][2 * v + h] = pack_f16x2(p0, p1);
+              if constexpr (kWide) {
+                const float2 hi = unpack_f16x2(pa[0][kk][2 * v + h]);
+                pa[1][kk][2 * v + h] = pack_f16x2(p0 - hi.x, p1 - hi.y);
+              }
+            }
+        }
+        // ---- move the output to the new maximum and unit
+        const float r0 = alpha[0] * (step == 0 ? ratio : 1.f), r1 = alpha[1] * (step == 0 ? ratio : 1.f);
+        if (__any_sync(0xffffffffu, r0 != 1.f || r1 != 1.f)) {
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            o[c][0] *= r0;
+            o[c][1] *= r0;
+            o[c][4] *= r0;
+            o[c][5] *= r0;
+            o[c][2] *= r1;
+            o[c][3] *= r1;
+            o[c][6] *= r1;
+            o[c][7] *= r1;
+          }
+        }
+        // ---- output
+#pragma unroll
+        for (int kk = 0; kk < kNt / 2; ++kk) {
+          const int key = step * kKeys + 16 * kk;
+          uint32_t seen0 = ~0u, seen1 = ~0u;
+          if (edge) {
+            // rows past the sequence hold anything: their codes are zeroed (0 x
+            // NaN would reach every row).  This lane's keys: 2 tq, 2 tq + 1 (+ 8)
+            const int k0 = blk * kBlk + key + 2 * tq;
+            seen0 = (k0 < w.len ? 0xffffu : 0u) | (k0 + 1 < w.len ? 0xffff0000u : 0u);
+            seen1 = (k0 + 8 < w.len ? 0xffffu : 0u) | (k0 + 9 < w.len ? 0xffff0000u : 0u);
+          }
+#pragma unroll
+          for (int c2 = 0; c2 < kC / 2; ++c2) {
+            uint32_t r[4];
+            ldsm4_t(vt + tile_off<HD>(key + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)), r);
+            if (edge) {
+              r[0] &= seen0;
+              r[1] &= seen1;
+              r[2] &= seen0;
+              r[3] &= seen1;
+              // a NaN that not every row sees is taken out of the product, and the
+              // rows that do see its key get NaN: visibility (1 or 0) times
+              // occurrence, a product of its own
+              const uint32_t bad[4] = {nan_bytes(r[0]), nan_bytes(r[1]), nan_bytes(r[2]), nan_bytes(r[3])};
+              if (__any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u)) {
+                uint32_t va[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const int k0 = blk * kBlk + key + 2 * tq + 8 * (z >> 1), n = lim[z & 1];
+                  va[z] = (k0 < n ? 0x3c00u : 0u) | (k0 + 1 < n ? 0x3c000000u : 0u);
+                }
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                  // bytes (key, dim): (0, even), (0, odd), (1, even), (1, odd)
+                  const uint32_t b0 = bad[2 * ch], b1 = bad[2 * ch + 1];
+                  float* oc = o[2 * c2 + ch];
+#pragma unroll
+                  for (int od = 0; od < 2; ++od) {
+                    const uint32_t sel = od ? 0x3311u : 0x2200u;
+                    float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(hit, va, __byte_perm(b0, 0u, sel) & 0x3c003c00u, __byte_perm(b1, 0u, sel) & 0x3c003c00u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                      if (hit[j] > 0.f) oc[4 * od + j] = NAN;
+                  }
+                  r[2 * ch] &= ~b0;
+                  r[2 * ch + 1] &= ~b1;
+                }
+              }
+            }
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+              const uint32_t y0 = __byte_perm(r[2 * ch], 0u, 0x3120), y1 = __byte_perm(r[2 * ch + 1], 0u, 0x3120);
+              const uint32_t e0v = e4m3x2_to_f16x2((uint16_t)(y0 & 0xffffu)), e1v = e4m3x2_to_f16x2((uint16_t)(y1 & 0xffffu));
+              const uint32_t d0v = e4m3x2_to_f16x2((uint16_t)(y0 >> 16)), d1v = e4m3x2_to_f16x2((uint16_t)(y1 >> 16));
+              float* oc = o[2 * c2 + ch];
+              mma_f16(oc, pa[0][kk], e0v, e1v);
+              mma_f16(oc + 4, pa[0][kk], d0v, d1v);
+              if constexpr (kWide) {
+                mma_f16(oc, pa[1][kk], e0v, e1v);
+                mma_f16(oc + 4, pa[1][kk], d0v, d1v);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+    }
+    // ---- the item's rows: each warp's normalised output, maximum and sum
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float l = l_run[h];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int r = warp * 16 + gq + 8 * h;
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+        *reinterpret_cast<float4*>(Ow + r * SM::kRowF + 16 * c + 4 * tq) =
+            make_float4(o[c][2 * h] * inv * unit, o[c][4 + 2 * h] * inv * unit, o[c][2 * h + 1] * inv * unit,
+                        o[c][5 + 2 * h] * inv * unit);
+      if (tq == 0) {
+        MLw[2 * r] = m_run[h];
+        MLw[2 * r + 1] = l;
+      }
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    // ---- joined over the key-splitting warps: to the output, or to this CTA's
+    // first (slot 0: the item began at or before the run) or last partial
+    const int part = 2 * blockIdx.x + (u != u0 ? 1 : 0);
+    const int irows = 16 * a.nm;
+    for (int j = tid; j < irows * (HD / 4); j += kWarps * 32) {
+      const int rr = j / (HD / 4), d = j % (HD / 4) * 4;
+      const int r = w.mg * irows + rr;
+      if (r >= rows) continue;
+      const int first = rr;  // row rr % 16 of warp rr / 16; the next key part is nm warps on
+      float M = -INFINITY;
+      for (int k = 0; k < kw; ++k) M = fmaxf(M, MLw[2 * (first + 16 * a.nm * k)]);
+      const float ms = M == -INFINITY ? 0.f : M;
+      float W = 0.f;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < kw; ++k) {
+        const int at = first + 16 * a.nm * k;
+        const float l = MLw[2 * at + 1];
+        if (l == 0.f) continue;
+        const float e = l * ex2(MLw[2 * at] - ms);
+        const float4 v = *reinterpret_cast<const float4*>(Ow + at * SM::kRowF + d);
+        W += e;
+        y.x = fmaf(e, v.x, y.x);
+        y.y = fmaf(e, v.y, y.y);
+        y.z = fmaf(e, v.z, y.z);
+        y.w = fmaf(e, v.w, y.w);
+      }
+      const float inv = W == 0.f ? 0.f : 1.f / W;
+      y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+      if (whole) {
+        const int t = row_tok(a, r);
+        store_row4(reinterpret_cast<T*>(a.out) +
+                       (((size_t)w.b * a.ntok + t) * a.nh + w.g * G + (r - t * G)) * HD + d,
+                   y);
+      } else {
+        const size_t at = (size_t)part * irows + rr;
+        *reinterpret_cast<float4*>(a.part + at * HD + d) = y;
+        if (d == 0)
+          *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * irows * HD + 2 * at) = make_float2(M, W);
+      }
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    u += n;
+    i += n;
+    w.blk += n;
+    if (u < u1) w.next_item(a);
+  }
+}
+
+// Joins the partial rows of the items that a run's end cut, in the runs' order,
+// and zeroes the rows of items without a visible key.  One CTA per row.
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) kv8_join_kernel(const Kv8Attn a) {
+  constexpr int kLanes = HD / 4, kGroups = 128 / kLanes;
+  constexpr int kMost = kCtasMax;  // an item's partial rows: at most one per CTA of the split kernel
+  __shared__ float s_w[kMost], s_m[kMost];
+  __shared__ int s_int[8];
+  __shared__ float s_red[8];
+  __shared__ float4 s_o[128];
+  pdl_launch_dependents();
+  const int r = blockIdx.x, g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int irows = 16 * a.nm, mg = r / irows, rr = r - mg * irows;
+  const int G = a.nh / a.nkv, t = row_tok(a, r);
+  const int e = b * a.mgroups + mg;
+  int before, e0, e1;
+  // (the lengths are the caller's, not the split kernel's: they may be read before it ends ...)
+  pdl_wait();  // (... but not before the kernel that wrote them; its partials need the wait anyhow)
+  const int total = scan_entries(a, tid, 128, s_int, &before, &e0, &e1);
+  if (e0 <= e && e < e1) {
+    for (int x = e0; x < e; ++x) before += entry_units(a, x);
+    s_int[4] = before;
+  }
+  __syncthreads();
+  T* out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.ntok + t) * a.nh + g * G + (r - t * G)) * HD;
+  const int nb = item_blocks(a, seq_len(a, b), mg);
+  const int lane = tid % kLanes, grp = tid / kLanes;
+  if (nb == 0) {
+    if (grp == 0) store_row4(out + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f));
+    return;
+  }
+  const int run = run_units(a, total), us = s_int[4] + g * nb;
+  const int c0 = us / run, n = (us + nb - 1) / run - c0 + 1;
+  if (n == 1) return;  // the split kernel has written it
+  const float* ml = a.part + (size_t)2 * a.ctas * irows * HD;
+  auto row_of = [&](int i) { return (size_t)(2 * (c0 + i) + (us > (c0 + i) * run ? 1 : 0)) * irows + rr; };
+  float M = -INFINITY;
+  for (int i = tid; i < n; i += 128) {
+    const float2 v = *reinterpret_cast<const float2*>(ml + 2 * row_of(i));
+    s_m[i] = v.x;
+    s_w[i] = v.y;
+    M = fmaxf(M, v.x);
+  }
+  M = warp_max(M);
+  if ((tid & 31) == 0) s_red[tid >> 5] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  const float ms = M == -INFINITY ? 0.f : M;
+  float W = 0.f;
+  for (int i = tid; i < n; i += 128) {
+    const float x = s_w[i] == 0.f ? 0.f : s_w[i] * ex2(s_m[i] - ms);
+    s_w[i] = x;
+    W += x;
+  }
+  W = warp_sum(W);
+  if ((tid & 31) == 0) s_red[4 + (tid >> 5)] = W;
+  __syncthreads();
+  W = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = grp; i < n; i += kGroups) {
+    const float x = s_w[i];
+    if (x == 0.f) continue;
+    const float4 v = *reinterpret_cast<const float4*>(a.part + row_of(i) * HD + 4 * lane);
+    y.x = fmaf(x, v.x, y.x);
+    y.y = fmaf(x, v.y, y.y);
+    y.z = fmaf(x, v.z, y.z);
+    y.w = fmaf(x, v.w, y.w);
+  }
+  s_o[tid] = y;
+  __syncthreads();
+  if (grp == 0) {
+    for (int k = 1; k < kGroups; ++k) {
+      const float4 v = s_o[k * kLanes + lane];
+      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+    }
+    const float inv = W == 0.f ? 0.f : 1.f / W;
+    store_row4(out + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+  }
+}
+
+template <typename T, int HD>
+q2_status split_t(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaStream_t st) {
+  using SM = SplitSmem<T, HD>;
+  auto* kernel = kv8_split_kernel<T, HD>;
+  Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
+  CUtensorMap km, vm;
+  const uint64_t rows = (uint64_t)a.batch * a.nkv * a.max_seq;
+  Q2_TRY(make_tmap_2d_u8(&km, kc, rows, HD, HD, kBlk, HD, HD));
+  Q2_TRY(make_tmap_2d_u8(&vm, vc, rows, HD, HD, kBlk, HD, HD));
+  Q2_LAUNCH(kernel, dim3(a.ctas), dim3(kThreads), SM::kTotal, st, true, a, km, vm);
+  Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(a.ntok * (a.nh / a.nkv), a.nkv, a.batch), dim3(128), 0, st, true, a);
   return Q2_OK;
 }
 
-q2_status attn(const Kv8Attn& a, int hd, int dtype, cudaStream_t st) {
-  return dtype == Q2_BF16 ? simple_t<__nv_bfloat16>(a, hd, st) : simple_t<float>(a, hd, st);
+template <typename T>
+q2_status split(const Kv8Attn& a, int hd, const uint8_t* kc, const uint8_t* vc, cudaStream_t st) {
+  switch (hd) {
+    case 32: return split_t<T, 32>(a, kc, vc, st);
+    case 64: return split_t<T, 64>(a, kc, vc, st);
+    default: return split_t<T, 128>(a, kc, vc, st);
+  }
+}
+
+// m-tiles per item, items per kv head, CTAs and workspace of the split kernel.
+struct SplitPlan {
+  int nm, mgroups, ctas;
+  size_t bytes;
+};
+SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd, int dtype) {
+  SplitPlan p;
+  const int mtiles = ceil_div((long long)(ntok * (nh / nkv)), 16);
+  p.nm = mtiles > 2 ? 4 : mtiles;
+  p.mgroups = ceil_div(mtiles, p.nm);
+  p.ctas = num_sms() * (dtype == Q2_BF16 ? 2 : 1);  // all resident at once
+  if (p.ctas > kCtasMax) p.ctas = kCtasMax;
+  p.bytes = (size_t)2 * p.ctas * 16 * p.nm * (hd + 2) * sizeof(float);
+  return p;
+}
+
+q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
+               cudaStream_t st) {
+  const SplitPlan p = split_plan(a.ntok, a.nh, a.nkv, hd, dtype);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < p.bytes) {
+    set_error("kv8 attention: the workspace is NULL, not 256-byte aligned or smaller than "
+              "q2_kv8_attention_workspace says");
+    return Q2_ERR_INVALID_ARG;
+  }
+  if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 30)) {
+    set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^30");
+    return Q2_ERR_SHAPE;
+  }
+  a.nm = p.nm;
+  a.mgroups = p.mgroups;
+  a.ctas = p.ctas;
+  a.part = static_cast<float*>(ws);
+  const auto* k = static_cast<const uint8_t*>(kc);
+  const auto* v = static_cast<const uint8_t*>(vc);
+  return dtype == Q2_BF16 ? split<__nv_bfloat16>(a, hd, k, v, st) : split<float>(a, hd, k, v, st);
 }
 
 }  // namespace
@@ -135,13 +800,12 @@ q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, c
   Q2_CHECK_ARG(lens, Q2_ERR_INVALID_ARG, "kv8_attention: NULL lens");
   int* flag = op_error_flag();
   Q2_CHECK_ARG(flag, Q2_ERR_CUDA, "cannot resolve the device error flag");
-  Q2_CHECK_ARG(workspace && workspace_bytes >= 256, Q2_ERR_INVALID_ARG, "kv8_attention: the workspace is too small");
-  Kv8Attn a;
+  Q2_CHECK_ARG((unsigned long long)batch * nkv * max_seq < (1ull << 31), Q2_ERR_SHAPE,
+               "kv8_attention: need batch * nkv * max_seq < 2^31");
+  Kv8Attn a = {};
   a.q = q;
   a.q_seq_stride = q_strides ? q_strides[0] : (long long)(ntok * nh * hd);
   a.q_tok_stride = q_strides ? q_strides[1] : (long long)(nh * hd);
-  a.kc = static_cast<const uint8_t*>(kc);
-  a.vc = static_cast<const uint8_t*>(vc);
   a.ks = ks;
   a.vs = vs;
   a.lens = lens;
@@ -155,7 +819,7 @@ q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, c
   a.scale = scale;
   a.out = out;
   a.err = flag;
-  return attn(a, (int)hd, dtype, as_stream(stream));
+  return attn(a, (int)hd, dtype, kc, vc, workspace, workspace_bytes, as_stream(stream));
 }
 
 q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const void* vc, const float* ks,
@@ -171,14 +835,12 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
   Q2_KV8_ATTN_PTRS("kv8_self_attention");
   int* flag = op_error_flag();
   Q2_CHECK_ARG(flag, Q2_ERR_CUDA, "cannot resolve the device error flag");
-  Q2_CHECK_ARG(workspace && workspace_bytes >= 256, Q2_ERR_INVALID_ARG,
-               "kv8_self_attention: the workspace is too small");
-  Kv8Attn a;
+  Q2_CHECK_ARG((unsigned long long)nkv * max_seq < (1ull << 31), Q2_ERR_SHAPE,
+               "kv8_self_attention: need nkv * max_seq < 2^31");
+  Kv8Attn a = {};
   a.q = q;
   a.q_seq_stride = 0;
   a.q_tok_stride = (long long)(nh * hd);
-  a.kc = static_cast<const uint8_t*>(kc);
-  a.vc = static_cast<const uint8_t*>(vc);
   a.ks = ks;
   a.vs = vs;
   a.lens = nullptr;
@@ -192,7 +854,7 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
   a.scale = scale;
   a.out = out;
   a.err = flag;
-  return attn(a, (int)hd, dtype, as_stream(stream));
+  return attn(a, (int)hd, dtype, kc, vc, workspace, workspace_bytes, as_stream(stream));
 }
 
 q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len, size_t nh, size_t nkv, size_t hd,
@@ -201,10 +863,10 @@ q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len
   const size_t max_seq = 1;
   Q2_KV8_ATTN_CHECK("kv8_attention_workspace");
   Q2_CHECK_ARG(bytes, Q2_ERR_INVALID_ARG, "kv8_attention_workspace: NULL bytes");
+  Q2_CHECK_ARG(ntok < 65536, Q2_ERR_SHAPE, "kv8_attention_workspace: need ntok < 65536");
   (void)batch;
-  (void)ntok;
   (void)total_len;
-  *bytes = 256;
+  *bytes = ntok ? split_plan(ntok, nh, nkv, hd, dtype).bytes : 0;
   return Q2_OK;
 }
 
