@@ -4,18 +4,21 @@
 // query rows of a kv head (ntok rows x nh / nkv heads) go on the M side of
 // mma.sync m16n8k16 (16 rows an m-tile, up to four m-tiles a work item), keys
 // on N for the scores, head dims on N for the output.  A work item is (sequence,
-// m-tiles, kv head); its unit of work is one block of 64 keys -- one scale of K
-// and one of V.  All items' blocks, in order, are dealt to a grid of resident
-// CTAs in equal runs (lengths are read on the device), so ragged batches and a
-// single long sequence load every SM alike; an item cut by a run's end leaves
-// partial results that a second kernel joins in order (the same result every
-// time).
+// m-tiles, kv head); its unit of work is 32 keys, half a block.  All items'
+// units, in order, are dealt to a grid of resident CTAs in equal runs (lengths
+// are read on the device), so ragged batches and a single long sequence load
+// every SM alike; an item cut by a run's end leaves partial results that a
+// second kernel joins in order (the same result every time).
 //
-// Bound by HBM (a byte per cached element): 64-key K and V tiles arrive by TMA
-// in a ring (swizzled to the head's row length) fed by one warp; four warps
-// consume, a block at a time each (or, with several m-tiles, one m-tile each of
-// the same block).  e4m3 values are exact in fp16 and Blackwell converts two
-// per instruction, so the products run in fp16 with fp32 accumulation:
+// Bound by HBM (a byte per cached element): a unit's K and V rows arrive by TMA
+// (swizzled to the head's row length).  Four warps a CTA; the nm warps that
+// share an item's units (one m-tile each) share 3 nm slots, a warp with an
+// m-tile of its own has three: its next two units are in flight while it
+// computes.  (With whole blocks and one ring for the CTA a warp's next tile
+// could only start when its last was done: 48 us instead of KV8_B64_US for 64
+// sequences of up to 4096 positions.)  e4m3 values are exact in fp16 and
+// Blackwell converts two per instruction, so the products run in fp16 with
+// fp32 accumulation:
 //   scores  a lane's 32 contiguous bytes of a key row (16-byte loads, no bank
 //           conflicts under the swizzle) feed eight MMAs: the order of the dims
 //           inside a dot product is free, the query's fragments take the same;
@@ -40,9 +43,10 @@ namespace {
 
 constexpr int kBlk = Q2_KV8_BLOCK;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWarps = 4;                       // consumers
-constexpr int kThreads = (kWarps + 1) * 32;     // and the producer
-constexpr int kRing = 4;                        // a multiple of kWarps: a slot always meets the same warps
+constexpr int kKeys = 32;                       // keys per unit
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kDepth = 3;                       // slots per warp
 constexpr int kCtasMax = 512;
 constexpr float kPBias = 14.f;                  // p <= 2^14 in fp16
 
@@ -54,6 +58,8 @@ struct Kv8Attn {
   const int32_t* lens;  // [batch] keys of each sequence; null: fixed_len
   int fixed_len;
   int batch, ntok, nh, nkv, max_seq, nblk;
+  int group;      // nh / nkv
+  unsigned magic; // ceil(2^32 / group): r / group = umulhi(r, magic) for group > 1
   int nm;       // m-tiles of an item: 1, 2 or 4
   int mgroups;  // items of a (sequence, kv head)
   float scale;
@@ -69,27 +75,28 @@ __device__ __forceinline__ int seq_len(const Kv8Attn& a, int b) {
   const int n = a.lens ? a.lens[b] : a.fixed_len;
   return n > a.max_seq || n < 0 ? 0 : n;
 }
-// Query token of row r of a kv head's rows.
-__device__ __forceinline__ int row_tok(const Kv8Attn& a, int r) { return r / (a.nh / a.nkv); }
-// Blocks that an item's rows see (the last row sees the most).
-__device__ __forceinline__ int item_blocks(const Kv8Attn& a, int len, int mg) {
-  const int rows = a.ntok * (a.nh / a.nkv);
-  const int last = min(rows, (mg + 1) * a.nm * 16) - 1;
+// Query token of row r of a kv head's rows (r < 2^20: the rounding of the magic
+// number adds less than r / 2^29 < 1 / group).
+__device__ __forceinline__ int row_tok(const Kv8Attn& a, int r) {
+  return a.group == 1 ? r : (int)__umulhi((unsigned)r, a.magic);
+}
+// Units that an item's rows see (the last row sees the most).
+__device__ __forceinline__ int item_units(const Kv8Attn& a, int len, int mg) {
+  const int last = min(a.ntok * a.group, (mg + 1) * a.nm * 16) - 1;
   const int keys = max(0, len - a.ntok + 1 + row_tok(a, last));
-  return (keys + kBlk - 1) / kBlk;
+  return (keys + kKeys - 1) / kKeys;
 }
 
 // Entries e = (sequence, m-group), e = b * mgroups + mg, hold nkv items of
-// item_blocks() units each.
+// item_units() units each.
 __device__ __forceinline__ int entry_units(const Kv8Attn& a, int e) {
-  const int b = e / a.mgroups;
-  return a.nkv * item_blocks(a, seq_len(a, b), e - b * a.mgroups);
+  const int b = a.mgroups == 1 ? e : e / a.mgroups;
+  return a.nkv * item_units(a, seq_len(a, b), e - b * a.mgroups);
 }
-// Every thread of the CTA (n, a multiple of 32) takes entries [*e0, *e1) and gets
-// the units before them; returns all entries' units.
-__device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int n, int* s_warp, int* mine_before,
-                                            int* e0, int* e1) {
-  const int entries = a.batch * a.mgroups, per = (entries + n - 1) / n;
+// Every thread of the CTA (128) takes entries [*e0, *e1) and gets the units
+// before them; returns all entries' units.
+__device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int* s_warp, int* before, int* e0, int* e1) {
+  const int entries = a.batch * a.mgroups, per = (entries + kThreads - 1) / kThreads;
   *e0 = min(entries, tid * per);
   *e1 = min(entries, *e0 + per);
   int sum = 0;
@@ -103,14 +110,15 @@ __device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int n, in
   if ((tid & 31) == 31) s_warp[tid >> 5] = inc;
   __syncthreads();
   int base = 0, total = 0;
-  for (int w = 0; w < n / 32; ++w) {
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
     if (w < (tid >> 5)) base += s_warp[w];
     total += s_warp[w];
   }
-  *mine_before = base + inc - sum;
+  *before = base + inc - sum;
   return total;
 }
-// Units per CTA: equal runs, at least one block per key-splitting warp.
+// Units per CTA: equal runs, at least one unit per key-splitting warp.
 __device__ __forceinline__ int run_units(const Kv8Attn& a, int total) {
   return max((total + a.ctas - 1) / a.ctas, kWarps / a.nm);
 }
@@ -126,7 +134,7 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
 }
 
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* x, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -135,7 +143,8 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* x, uint32_t b0
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr));
+               : "r"(addr)
+               : "memory");
 }
 template <int BYTES>
 __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
@@ -175,67 +184,91 @@ __device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
 
 template <typename T, int HD>
 struct SplitSmem {
-  static constexpr size_t kTile = (size_t)kBlk * HD;
+  static constexpr size_t kTile = (size_t)kKeys * HD;
   static constexpr size_t kSlot = 2 * kTile;
-  // a segment's rows of the four warps, rows 16 floats longer against conflicts
+  // a warp's rows at an item's end, over its share of the slots (free then);
+  // rows 16 floats longer against conflicts
   static constexpr int kRowF = HD + 16;
-  static constexpr size_t kO = kRing * kSlot;
-  static constexpr size_t kML = kO + (size_t)kWarps * 16 * kRowF * 4;
-  static constexpr size_t kBars = kML + (size_t)kWarps * 16 * 2 * 4;
-  static constexpr size_t kInts = kBars + 2 * kRing * 8;
+  static constexpr size_t kShare = kDepth * kSlot > 16 * kRowF * 4 ? kDepth * kSlot : (16 * kRowF * 4 + 1023) / 1024 * 1024;
+  static constexpr size_t kML = kWarps * kShare;
+  static constexpr size_t kNan = kML + (size_t)kWarps * 16 * 2 * 4;  // per warp: first NaN position of each dim
+  static constexpr size_t kBars = kNan + (size_t)kWarps * HD * 4;
+  static constexpr size_t kInts = kBars + 2 * kWarps * kDepth * 8;
   static constexpr size_t kTotal = kInts + 16 * 4 + 1024;
 };
 
-// Walks a CTA's units: item by item, block by block.
+// Walks a CTA's units: item by item.
 struct UnitWalk {
-  int e, b, mg, g, len, nb, blk;  // entry, its sequence and m-group, kv head, keys, blocks of an item, block
+  int e, b, mg, g, len, nu, at;  // entry, its sequence and m-group, kv head, keys, units of an item, next unit
   __device__ __forceinline__ void entry_of(const Kv8Attn& a) {
-    b = e / a.mgroups;
+    b = a.mgroups == 1 ? e : e / a.mgroups;
     mg = e - b * a.mgroups;
     len = seq_len(a, b);
-    nb = item_blocks(a, len, mg);
+    nu = item_units(a, len, mg);
   }
   __device__ __forceinline__ void seek(const Kv8Attn& a, int entry, int rem) {
     e = entry;
     entry_of(a);
-    g = rem / nb;
-    blk = rem - g * nb;
+    g = rem / nu;
+    at = rem - g * nu;
   }
-  // to the first block of the next item (there is one)
+  // to the first unit of the next item (there is one)
   __device__ __forceinline__ void next_item(const Kv8Attn& a) {
-    blk = 0;
+    at = 0;
     if (++g == a.nkv) {
       g = 0;
       do {
         ++e;
         entry_of(a);
-      } while (nb == 0);
+      } while (nu == 0);
     }
   }
 };
 
+// The V rows [row0, row1) of a 32-row tile in shared memory: rows from `stale`
+// on are zeroed (they lie past the sequence and may hold anything; 0 x NaN would
+// reach every query row); in the others the NaN codes are looked for.  first[d]
+// becomes the lowest position of a NaN in dim d (pos0: the tile's first
+// position).  Returns whether there was one.
+template <int HD>
+__device__ __noinline__ bool prepare_edge(uint8_t* vt, int stale, bool look, int pos0, int* first, int lane) {
+  bool any = false;
+  for (int i = lane; i < kKeys * HD / 16; i += 32) {
+    const int r = i / (HD / 16), c = i % (HD / 16);
+    uint4* p = reinterpret_cast<uint4*>(vt + tile_off<HD>(r, c));
+    if (r >= stale) {
+      *p = make_uint4(0u, 0u, 0u, 0u);
+    } else if (look) {
+      const uint4 v = *p;
+      const uint32_t w[4] = {nan_bytes(v.x), nan_bytes(v.y), nan_bytes(v.z), nan_bytes(v.w)};
+      if (w[0] | w[1] | w[2] | w[3]) {
+        any = true;
+        for (int j = 0; j < 16; ++j)
+          if ((w[j >> 2] >> (8 * (j & 3))) & 1u) atomicMin(first + 16 * c + j, pos0 + r);
+      }
+    }
+  }
+  return __any_sync(0xffffffffu, any);
+}
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 2)
     kv8_split_kernel(const Kv8Attn a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using SM = SplitSmem<T, HD>;
   constexpr bool kWide = sizeof(T) == 4;  // fp32: two fp16 parts of q and of p
   constexpr int kTerms = kWide ? 2 : 1;
-  constexpr int kKeys = kWide ? 32 : 64;  // keys per softmax step (fp32's extra parts need the registers)
   constexpr int kNt = kKeys / 8, kC = HD / 16;
   extern __shared__ __align__(1024) uint8_t kv8_smem_raw[];
   uint8_t* smem = kv8_smem_raw + ((1024u - (smem_u32(kv8_smem_raw) & 1023u)) & 1023u);
-  float* Ow = reinterpret_cast<float*>(smem + SM::kO);
   float* MLw = reinterpret_cast<float*>(smem + SM::kML);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kBars);
-  uint64_t* empty = full + kRing;
+  uint64_t* empty = full + kWarps * kDepth;
   int* s_int = reinterpret_cast<int*>(smem + SM::kInts);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], a.nm);
-    }
+  if (tid < kWarps * kDepth) {
+    mbar_init(&full[tid], 1);
+    mbar_init(&empty[tid], a.nm);
     fence_mbar_init();
   }
   pdl_launch_dependents();
@@ -243,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
 
   // this CTA's run of units
   int before, e0, e1;
-  const int total = scan_entries(a, tid, kThreads, s_int + 4, &before, &e0, &e1);
+  const int total = scan_entries(a, tid, s_int + 4, &before, &e0, &e1);
   const int run = run_units(a, total);
   const int u0 = (int)min((long long)blockIdx.x * run, (long long)total), u1 = min(total, u0 + run);
   if (u0 < u1)
@@ -263,46 +296,54 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
   UnitWalk w;
   w.seek(a, s_int[0], s_int[1]);
 
-  if (warp == kWarps) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int s = 0;
-      uint32_t ph = 0;
-      for (int u = u0; u < u1;) {
-        const int row = (w.b * a.nkv + w.g) * a.max_seq;
-        for (; w.blk < w.nb && u < u1; ++w.blk, ++u) {
-          uint8_t* st = smem + s * SM::kSlot;
-          if (!tc_wait_asleep(&empty[s], ph ^ 1u)) atomicOr(a.err, kErrTimeout);
-          mbar_arrive_expect_tx(&full[s], (uint32_t)SM::kSlot);
-          tma_load_2d(st, &kmap, 0, row + w.blk * kBlk, &full[s]);
-          tma_load_2d(st + SM::kTile, &vmap, 0, row + w.blk * kBlk, &full[s]);
-          if (++s == kRing) {
-            s = 0;
-            ph ^= 1u;
-          }
-        }
-        if (u < u1) w.next_item(a);
-      }
-    }
-    return;
-  }
-
-  // -------------------------------------------------------------- consumers
   const int kw = kWarps / a.nm;            // warps that split the keys of an m-tile
   const int mt = warp % a.nm, kg = warp / a.nm;
   const int gq = lane >> 2, tq = lane & 3;
-  const int G = a.nh / a.nkv, rows = a.ntok * G;
+  const int G = a.group, rows = a.ntok * G;
   const int mi = lane >> 3, mr = lane & 7;
   const float sl2 = a.scale * kLog2e;
-  int i = 0;  // units of this CTA before the current item
+  // the slots of this warp's group (the nm warps of one kg), a ring; the warp
+  // of m-tile 0 fills them
+  const int slots = kDepth * a.nm, slot0 = kg * slots;
+  uint8_t* ring = smem + (size_t)kg * a.nm * SM::kShare;
+  int fill_s = 0, use_s = 0;
+  uint32_t fill_ph = 0, use_ph = 0;
+  int* first_nan = reinterpret_cast<int*>(smem + SM::kNan) + warp * HD;
+
   for (int u = u0; u < u1;) {
-    const int n = min(w.nb - w.blk, u1 - u);       // units of this item here
-    const bool whole = n == w.nb;
+    const int n = min(w.nu - w.at, u1 - u);        // units of this item here
+    const bool whole = n == w.nu;
     const int m0 = (w.mg * a.nm + mt) * 16;        // the m-tile's first row
     const bool two = m0 + 8 < rows;                // rows 8..15 exist
     const size_t head = (size_t)w.b * a.nkv + w.g;
     const float* ksp = a.ks + head * a.nblk;
     const float* vsp = a.vs + head * a.nblk;
+    const int tile_row = (int)head * a.max_seq;
+
+    // units kg, kg + kw, ... of the n are this group's
+    int fill = kg;
+    auto fill_next = [&]() {
+      if (fill >= n) return;
+      if (!tc_wait_asleep(&empty[slot0 + fill_s], fill_ph ^ 1u)) atomicOr(a.err, kErrTimeout);
+      uint64_t* bar = &full[slot0 + fill_s];
+      uint8_t* st = ring + (size_t)fill_s * SM::kSlot;
+      const int row = tile_row + (w.at + fill) * kKeys;
+      mbar_arrive_expect_tx(bar, (uint32_t)SM::kSlot);
+      tma_load_2d(st, &kmap, 0, row, bar);
+      tma_load_2d(st + SM::kTile, &vmap, 0, row, bar);
+      fill += kw;
+      if (++fill_s == slots) {
+        fill_s = 0;
+        fill_ph ^= 1u;
+      }
+    };
+    if (mt == 0 && lane == 0)
+      for (int i = 0; i < slots; ++i) fill_next();
+    float ks_n = 0.f, vs_n = 0.f;
+    if (kg < n) {
+      ks_n = __ldg(ksp + (w.at + kg) * kKeys / kBlk);
+      vs_n = __ldg(vsp + (w.at + kg) * kKeys / kBlk);
+    }
 
     // query fragments: rows gq and gq + 8, the lane's HD / 4 contiguous dims
     uint32_t qa[kTerms][HD / 16][4];
@@ -353,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     }
     // keys below every row's limit need no mask
     const int clear = w.len - a.ntok + 1 + row_tok(a, min(m0, rows - 1));
+    bool some_nan = false;  // first_nan is in use
 
     float o[kC][8];  // per chunk of 16 dims: even dims' tile, odd dims' tile
 #pragma unroll
@@ -362,63 +404,53 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
     float unit = 0.f, unit_max = 0.f;
 
-    // this warp's units of the item: CTA unit x with x % kw == kg
-    int x = i + (kg - i % kw + kw) % kw;
-    float ks_n = 0.f, vs_n = 0.f;
-    if (x < i + n) {
-      ks_n = __ldg(ksp + w.blk + x - i);
-      vs_n = __ldg(vsp + w.blk + x - i);
-    }
-    for (; x < i + n; x += kw) {
-      const int slot = x % kRing, blk = w.blk + x - i;
+    for (int x = kg; x < n; x += kw) {
+      const int key0 = (w.at + x) * kKeys;
       const float ksc = ks_n, vsc = vs_n;
-      if (x + kw < i + n) {
-        ks_n = __ldg(ksp + blk + kw);
-        vs_n = __ldg(vsp + blk + kw);
+      if (x + kw < n) {
+        ks_n = __ldg(ksp + (key0 + kw * kKeys) / kBlk);
+        vs_n = __ldg(vsp + (key0 + kw * kKeys) / kBlk);
       }
-      if (!tc_wait_asleep(&full[slot], (uint32_t)((x / kRing) & 1)) && lane == 0) atomicOr(a.err, kErrTimeout);
-      if (m0 >= rows) {  // an m-tile without rows (three of four)
-        if (lane == 0) mbar_arrive(&empty[slot]);
-        continue;
-      }
-      const uint32_t kt = smem_u32(smem + slot * SM::kSlot), vt = kt + (uint32_t)SM::kTile;
-      // the unit of this block's V scale (never 2^60 below the largest so far:
-      // the output in units of it stays in range)
-      unit_max = fmaxf(unit_max, vsc);
-      const float unit_new = fmaxf(fmaxf(vsc, unit_max * 0x1p-60f), 0x1p-126f);
-      const float ratio = unit_new == unit ? 1.f : unit / unit_new;
-      const float pf = vsc == unit_new ? 1.f : vsc / unit_new;
-      unit = unit_new;
-#pragma unroll
-      for (int step = 0; step < kBlk / kKeys; ++step) {
-        const int key0 = blk * kBlk + step * kKeys;
-        const bool edge = key0 + kKeys > clear;
-        // ---- scores
+      if (!tc_wait_asleep(&full[slot0 + use_s], use_ph) && lane == 0) atomicOr(a.err, kErrTimeout);
+      uint8_t* tile = ring + (size_t)use_s * SM::kSlot;
+      const uint32_t kt = smem_u32(tile), vt = kt + (uint32_t)SM::kTile;
+      if (m0 < rows) {  // (three m-tiles of four: the last has no rows)
+        // ---- scores: four key tiles side by side, so that no MMA waits for the last
         float s[kNt][4];
+        uint32_t kb[kNt][HD / 16];
 #pragma unroll
         for (int nt = 0; nt < kNt; ++nt) {
           s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-          const int r = step * kKeys + nt * 8 + gq;
-          uint32_t kb[HD / 16];
+          const int r = nt * 8 + gq;
           if constexpr (HD == 128) {
-            lds_words<16>(kt + tile_off<HD>(r, 2 * tq), kb);
-            lds_words<16>(kt + tile_off<HD>(r, 2 * tq + 1), kb + 4);
+            lds_words<16>(kt + tile_off<HD>(r, 2 * tq), kb[nt]);
+            lds_words<16>(kt + tile_off<HD>(r, 2 * tq + 1), kb[nt] + 4);
           } else if constexpr (HD == 64) {
-            lds_words<16>(kt + tile_off<HD>(r, tq), kb);
+            lds_words<16>(kt + tile_off<HD>(r, tq), kb[nt]);
           } else {
-            lds_words<8>(kt + tile_off<HD>(r, tq >> 1) + 8 * (tq & 1), kb);
+            lds_words<8>(kt + tile_off<HD>(r, tq >> 1) + 8 * (tq & 1), kb[nt]);
           }
+        }
 #pragma unroll
-          for (int j = 0; j < HD / 16; ++j) {
-            const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(kb[j] & 0xffffu));
-            const uint32_t b1 = e4m3x2_to_f16x2((uint16_t)(kb[j] >> 16));
+        for (int j = 0; j < HD / 16; ++j)
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) {
+            const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(kb[nt][j] & 0xffffu));
+            const uint32_t b1 = e4m3x2_to_f16x2((uint16_t)(kb[nt][j] >> 16));
             mma_f16(s[nt], qa[0][j], b0, b1);
             if constexpr (kWide) mma_f16(s[nt], qa[1][j], b0, b1);
           }
-        }
+        // ---- the unit of this block's V scale (never 2^60 below the largest so
+        // far: the output in units of it stays in range)
+        unit_max = fmaxf(unit_max, vsc);
+        const float unit_new = fmaxf(fmaxf(vsc, unit_max * 0x1p-60f), 0x1p-126f);
+        const float ratio = unit_new == unit ? 1.f : unit / unit_new;
+        const float pf = vsc == unit_new ? 1.f : vsc / unit_new;
+        unit = unit_new;
         // ---- softmax of rows gq (h = 0) and gq + 8 (h = 1)
+        const bool edge = key0 + kKeys > clear;
         uint32_t pa[kTerms][kNt / 2][4];
-        float alpha[2] = {1.f, 1.f};
+        float move[2] = {ratio, ratio};  // of the output: to the new maximum and unit
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 1 && !two) {
@@ -443,7 +475,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           const float mn = fmaxf(m_run[h], mx);
           const float ms = mn == -INFINITY ? 0.f : mn;
-          alpha[h] = ex2(m_run[h] - ms);
+          const float alpha = ex2(m_run[h] - ms);
+          move[h] *= alpha;
           m_run[h] = mn;
           float sum = 0.f;
 #pragma unroll
@@ -454,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
               s[nt][2 * h + j] = p;
               sum += p;
             }
-          l_run[h] = l_run[h] * alpha[h] + sum;
+          l_run[h] = l_run[h] * alpha + sum;
           if (pf != 1.f) {
 #pragma unroll
             for (int nt = 0; nt < kNt; ++nt) {
@@ -474,130 +507,112 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
               }
             }
         }
-        // ---- move the output to the new maximum and unit
-        const float r0 = alpha[0] * (step == 0 ? ratio : 1.f), r1 = alpha[1] * (step == 0 ? ratio : 1.f);
-        if (__any_sync(0xffffffffu, r0 != 1.f || r1 != 1.f)) {
+        if (__any_sync(0xffffffffu, move[0] != 1.f || move[1] != 1.f)) {
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            o[c][0] *= r0;
-            o[c][1] *= r0;
-            o[c][4] *= r0;
-            o[c][5] *= r0;
-            o[c][2] *= r1;
-            o[c][3] *= r1;
-            o[c][6] *= r1;
-            o[c][7] *= r1;
+          for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[c][j] *= move[(j >> 1) & 1];
+        }
+        // ---- rows past the sequence, NaN that not every row sees
+        bool drop_nan = false;
+        if (edge && (a.ntok > 1 || key0 + kKeys > w.len)) {
+          if (!some_nan) {
+            for (int d = lane; d < HD; d += 32) first_nan[d] = INT32_MAX;
+            __syncwarp();
           }
+          drop_nan = prepare_edge<HD>(tile + SM::kTile, w.len - key0, a.ntok > 1, key0, first_nan, lane);
+          some_nan |= drop_nan;
+          __syncwarp();
         }
         // ---- output
 #pragma unroll
         for (int kk = 0; kk < kNt / 2; ++kk) {
-          const int key = step * kKeys + 16 * kk;
-          uint32_t seen0 = ~0u, seen1 = ~0u;
-          if (edge) {
-            // rows past the sequence hold anything: their codes are zeroed (0 x
-            // NaN would reach every row).  This lane's keys: 2 tq, 2 tq + 1 (+ 8)
-            const int k0 = blk * kBlk + key + 2 * tq;
-            seen0 = (k0 < w.len ? 0xffffu : 0u) | (k0 + 1 < w.len ? 0xffff0000u : 0u);
-            seen1 = (k0 + 8 < w.len ? 0xffffu : 0u) | (k0 + 9 < w.len ? 0xffff0000u : 0u);
+          uint32_t r[kC / 2][4];
+#pragma unroll
+          for (int c2 = 0; c2 < kC / 2; ++c2)
+            ldsm4_t(vt + tile_off<HD>(16 * kk + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)), r[c2]);
+          if (drop_nan) {
+#pragma unroll
+            for (int c2 = 0; c2 < kC / 2; ++c2)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) r[c2][z] &= ~nan_bytes(r[c2][z]);
           }
 #pragma unroll
-          for (int c2 = 0; c2 < kC / 2; ++c2) {
-            uint32_t r[4];
-            ldsm4_t(vt + tile_off<HD>(key + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)), r);
-            if (edge) {
-              r[0] &= seen0;
-              r[1] &= seen1;
-              r[2] &= seen0;
-              r[3] &= seen1;
-              // a NaN that not every row sees is taken out of the product, and the
-              // rows that do see its key get NaN: visibility (1 or 0) times
-              // occurrence, a product of its own
-              const uint32_t bad[4] = {nan_bytes(r[0]), nan_bytes(r[1]), nan_bytes(r[2]), nan_bytes(r[3])};
-              if (__any_sync(0xffffffffu, (bad[0] | bad[1] | bad[2] | bad[3]) != 0u)) {
-                uint32_t va[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                  const int k0 = blk * kBlk + key + 2 * tq + 8 * (z >> 1), n = lim[z & 1];
-                  va[z] = (k0 < n ? 0x3c00u : 0u) | (k0 + 1 < n ? 0x3c000000u : 0u);
-                }
-#pragma unroll
-                for (int ch = 0; ch < 2; ++ch) {
-                  // bytes (key, dim): (0, even), (0, odd), (1, even), (1, odd)
-                  const uint32_t b0 = bad[2 * ch], b1 = bad[2 * ch + 1];
-                  float* oc = o[2 * c2 + ch];
-#pragma unroll
-                  for (int od = 0; od < 2; ++od) {
-                    const uint32_t sel = od ? 0x3311u : 0x2200u;
-                    float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(hit, va, __byte_perm(b0, 0u, sel) & 0x3c003c00u, __byte_perm(b1, 0u, sel) & 0x3c003c00u);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                      if (hit[j] > 0.f) oc[4 * od + j] = NAN;
-                  }
-                  r[2 * ch] &= ~b0;
-                  r[2 * ch + 1] &= ~b1;
-                }
-              }
-            }
-#pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
-              const uint32_t y0 = __byte_perm(r[2 * ch], 0u, 0x3120), y1 = __byte_perm(r[2 * ch + 1], 0u, 0x3120);
-              const uint32_t e0v = e4m3x2_to_f16x2((uint16_t)(y0 & 0xffffu)), e1v = e4m3x2_to_f16x2((uint16_t)(y1 & 0xffffu));
-              const uint32_t d0v = e4m3x2_to_f16x2((uint16_t)(y0 >> 16)), d1v = e4m3x2_to_f16x2((uint16_t)(y1 >> 16));
-              float* oc = o[2 * c2 + ch];
-              mma_f16(oc, pa[0][kk], e0v, e1v);
-              mma_f16(oc + 4, pa[0][kk], d0v, d1v);
-              if constexpr (kWide) {
-                mma_f16(oc, pa[1][kk], e0v, e1v);
-                mma_f16(oc + 4, pa[1][kk], d0v, d1v);
-              }
+          for (int c = 0; c < kC; ++c) {
+            // bytes (key, dim): (0, even), (0, odd), (1, even), (1, odd)
+            const uint32_t y0 = __byte_perm(r[c / 2][2 * (c & 1)], 0u, 0x3120);
+            const uint32_t y1 = __byte_perm(r[c / 2][2 * (c & 1) + 1], 0u, 0x3120);
+            const uint32_t e0v = e4m3x2_to_f16x2((uint16_t)(y0 & 0xffffu)), e1v = e4m3x2_to_f16x2((uint16_t)(y1 & 0xffffu));
+            const uint32_t d0v = e4m3x2_to_f16x2((uint16_t)(y0 >> 16)), d1v = e4m3x2_to_f16x2((uint16_t)(y1 >> 16));
+            mma_f16(o[c], pa[0][kk], e0v, e1v);
+            mma_f16(o[c] + 4, pa[0][kk], d0v, d1v);
+            if constexpr (kWide) {
+              mma_f16(o[c], pa[1][kk], e0v, e1v);
+              mma_f16(o[c] + 4, pa[1][kk], d0v, d1v);
             }
           }
         }
+        if (edge) fence_async_smem();  // zeroed rows before the slot's next copy
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (lane == 0) {
+        mbar_arrive(&empty[slot0 + use_s]);
+        if (mt == 0) fill_next();
+      }
+      __syncwarp();
+      if (++use_s == slots) {
+        use_s = 0;
+        use_ph ^= 1u;
+      }
     }
-    // ---- the item's rows: each warp's normalised output, maximum and sum
+
+    // ---- the item's rows: each warp's normalised output, maximum and sum, over
+    // its share of the slots (all consumed: its group's, once every warp is here)
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    float* Ow = reinterpret_cast<float*>(smem + (size_t)warp * SM::kShare);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float l = l_run[h];
       l += __shfl_xor_sync(0xffffffffu, l, 1);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int r = warp * 16 + gq + 8 * h;
+      const int r = gq + 8 * h;
+      if (some_nan) {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (first_nan[16 * c + 4 * tq + j] < lim[h]) o[c][2 * h + (j >> 1) + 4 * (j & 1)] = NAN;
+      }
 #pragma unroll
       for (int c = 0; c < kC; ++c)
         *reinterpret_cast<float4*>(Ow + r * SM::kRowF + 16 * c + 4 * tq) =
             make_float4(o[c][2 * h] * inv * unit, o[c][4 + 2 * h] * inv * unit, o[c][2 * h + 1] * inv * unit,
                         o[c][5 + 2 * h] * inv * unit);
       if (tq == 0) {
-        MLw[2 * r] = m_run[h];
-        MLw[2 * r + 1] = l;
+        MLw[2 * (16 * warp + r)] = m_run[h];
+        MLw[2 * (16 * warp + r) + 1] = l;
       }
     }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     // ---- joined over the key-splitting warps: to the output, or to this CTA's
     // first (slot 0: the item began at or before the run) or last partial
     const int part = 2 * blockIdx.x + (u != u0 ? 1 : 0);
-    const int irows = 16 * a.nm;
-    for (int j = tid; j < irows * (HD / 4); j += kWarps * 32) {
-      const int rr = j / (HD / 4), d = j % (HD / 4) * 4;
-      const int r = w.mg * irows + rr;
-      if (r >= rows) continue;
-      const int first = rr;  // row rr % 16 of warp rr / 16; the next key part is nm warps on
+    const int irows = 16 * a.nm, here = min(irows, rows - w.mg * irows);
+    for (int j = tid; j < here * (HD / 4); j += kThreads) {
+      const int rr = j / (HD / 4), d = j % (HD / 4) * 4;  // row rr % 16 of warp rr / 16; the next key part is nm warps on
       float M = -INFINITY;
-      for (int k = 0; k < kw; ++k) M = fmaxf(M, MLw[2 * (first + 16 * a.nm * k)]);
+      for (int k = 0; k < kw; ++k) M = fmaxf(M, MLw[2 * (rr + 16 * a.nm * k)]);
       const float ms = M == -INFINITY ? 0.f : M;
       float W = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int k = 0; k < kw; ++k) {
-        const int at = first + 16 * a.nm * k;
+        const int at = rr + 16 * a.nm * k;
         const float l = MLw[2 * at + 1];
         if (l == 0.f) continue;
         const float e = l * ex2(MLw[2 * at] - ms);
-        const float4 v = *reinterpret_cast<const float4*>(Ow + at * SM::kRowF + d);
+        const float4 v = *reinterpret_cast<const float4*>(
+            smem + (size_t)(at >> 4) * SM::kShare + ((at & 15) * SM::kRowF + d) * 4);
         W += e;
         y.x = fmaf(e, v.x, y.x);
         y.y = fmaf(e, v.y, y.y);
@@ -607,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
       const float inv = W == 0.f ? 0.f : 1.f / W;
       y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       if (whole) {
-        const int t = row_tok(a, r);
+        const int r = w.mg * irows + rr, t = row_tok(a, r);
         store_row4(reinterpret_cast<T*>(a.out) +
                        (((size_t)w.b * a.ntok + t) * a.nh + w.g * G + (r - t * G)) * HD + d,
                    y);
@@ -618,11 +633,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1)
           *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * irows * HD + 2 * at) = make_float2(M, W);
       }
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
     u += n;
-    i += n;
-    w.blk += n;
-    if (u < u1) w.next_item(a);
+    w.at += n;
+    if (u < u1) {
+      fence_async_smem();  // the rows before the slots' next copies
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      w.next_item(a);
+    }
   }
 }
 
@@ -639,26 +656,25 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const Kv8Attn a) {
   pdl_launch_dependents();
   const int r = blockIdx.x, g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int irows = 16 * a.nm, mg = r / irows, rr = r - mg * irows;
-  const int G = a.nh / a.nkv, t = row_tok(a, r);
+  const int G = a.group, t = row_tok(a, r);
   const int e = b * a.mgroups + mg;
   int before, e0, e1;
-  // (the lengths are the caller's, not the split kernel's: they may be read before it ends ...)
-  pdl_wait();  // (... but not before the kernel that wrote them; its partials need the wait anyhow)
-  const int total = scan_entries(a, tid, 128, s_int, &before, &e0, &e1);
+  pdl_wait();
+  const int total = scan_entries(a, tid, s_int, &before, &e0, &e1);
   if (e0 <= e && e < e1) {
     for (int x = e0; x < e; ++x) before += entry_units(a, x);
     s_int[4] = before;
   }
   __syncthreads();
   T* out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.ntok + t) * a.nh + g * G + (r - t * G)) * HD;
-  const int nb = item_blocks(a, seq_len(a, b), mg);
+  const int nu = item_units(a, seq_len(a, b), mg);
   const int lane = tid % kLanes, grp = tid / kLanes;
-  if (nb == 0) {
+  if (nu == 0) {
     if (grp == 0) store_row4(out + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
-  const int run = run_units(a, total), us = s_int[4] + g * nb;
-  const int c0 = us / run, n = (us + nb - 1) / run - c0 + 1;
+  const int run = run_units(a, total), us = s_int[4] + g * nu;
+  const int c0 = us / run, n = (us + nu - 1) / run - c0 + 1;
   if (n == 1) return;  // the split kernel has written it
   const float* ml = a.part + (size_t)2 * a.ctas * irows * HD;
   auto row_of = [&](int i) { return (size_t)(2 * (c0 + i) + (us > (c0 + i) * run ? 1 : 0)) * irows + rr; };
@@ -714,10 +730,10 @@ q2_status split_t(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaSt
   Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.batch * a.nkv * a.max_seq;
-  Q2_TRY(make_tmap_2d_u8(&km, kc, rows, HD, HD, kBlk, HD, HD));
-  Q2_TRY(make_tmap_2d_u8(&vm, vc, rows, HD, HD, kBlk, HD, HD));
+  Q2_TRY(make_tmap_2d_u8(&km, kc, rows, HD, HD, kKeys, HD, HD));
+  Q2_TRY(make_tmap_2d_u8(&vm, vc, rows, HD, HD, kKeys, HD, HD));
   Q2_LAUNCH(kernel, dim3(a.ctas), dim3(kThreads), SM::kTotal, st, true, a, km, vm);
-  Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(a.ntok * (a.nh / a.nkv), a.nkv, a.batch), dim3(128), 0, st, true, a);
+  Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(a.ntok * a.group, a.nkv, a.batch), dim3(128), 0, st, true, a);
   return Q2_OK;
 }
 
@@ -735,12 +751,12 @@ struct SplitPlan {
   int nm, mgroups, ctas;
   size_t bytes;
 };
-SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd, int dtype) {
+SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd) {
   SplitPlan p;
   const int mtiles = ceil_div((long long)(ntok * (nh / nkv)), 16);
   p.nm = mtiles > 2 ? 4 : mtiles;
   p.mgroups = ceil_div(mtiles, p.nm);
-  p.ctas = num_sms() * (dtype == Q2_BF16 ? 2 : 1);  // all resident at once
+  p.ctas = num_sms() * 2;  // all resident at once
   if (p.ctas > kCtasMax) p.ctas = kCtasMax;
   p.bytes = (size_t)2 * p.ctas * 16 * p.nm * (hd + 2) * sizeof(float);
   return p;
@@ -748,16 +764,18 @@ SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd, int dtype) {
 
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
                cudaStream_t st) {
-  const SplitPlan p = split_plan(a.ntok, a.nh, a.nkv, hd, dtype);
+  const SplitPlan p = split_plan(a.ntok, a.nh, a.nkv, hd);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < p.bytes) {
     set_error("kv8 attention: the workspace is NULL, not 256-byte aligned or smaller than "
               "q2_kv8_attention_workspace says");
     return Q2_ERR_INVALID_ARG;
   }
-  if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 30)) {
-    set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^30");
+  if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 29)) {
+    set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^29");
     return Q2_ERR_SHAPE;
   }
+  a.group = a.nh / a.nkv;
+  a.magic = a.group == 1 ? 0u : (unsigned)(((1ull << 32) + a.group - 1) / a.group);
   a.nm = p.nm;
   a.mgroups = p.mgroups;
   a.ctas = p.ctas;
@@ -866,7 +884,7 @@ q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len
   Q2_CHECK_ARG(ntok < 65536, Q2_ERR_SHAPE, "kv8_attention_workspace: need ntok < 65536");
   (void)batch;
   (void)total_len;
-  *bytes = ntok ? split_plan(ntok, nh, nkv, hd, dtype).bytes : 0;
+  *bytes = ntok ? split_plan(ntok, nh, nkv, hd).bytes : 0;
   return Q2_OK;
 }
 
