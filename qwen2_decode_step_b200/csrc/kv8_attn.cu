@@ -1,29 +1,29 @@
 // kv8_attn.cu -- attention over the 8-bit KV cache.
 //
-// Split kernel (any head dim, fp32 or bf16, one to many query rows).  The
-// query rows of a kv head (ntok rows x nh / nkv heads) go on the M side of
-// mma.sync m16n8k16 (16 rows an m-tile, up to four m-tiles a work item), keys
-// on N for the scores, head dims on N for the output.  A work item is (sequence,
-// m-tiles, kv head); its unit of work is 32 keys, half a block.  All items'
-// units, in order, are dealt to a grid of resident CTAs in equal runs (lengths
-// are read on the device), so ragged batches and a single long sequence load
-// every SM alike; an item cut by a run's end leaves partial results that a
-// second kernel joins in order (the same result every time).
+// Split kernel (any head dim, fp32 or bf16, one to many query rows).  Keys go on
+// the M side of mma.sync m16n8k16 for the scores and head dims for the output,
+// the query rows of a kv head (ntok rows x nh / nkv heads) on N, eight a tile:
+// S^T = K q^T, O^T = V^T P^T.  A decode step's at most eight rows fill one
+// tile; with the rows on M half of every MMA and of the accumulators stood
+// empty.  A warp takes NT row tiles (one, or two where there are more than
+// eight rows), up to four warps the rows of a work item (sequence, row group, kv
+// head); its unit of work is 32 keys, half a block.  All items' units, in
+// order, are dealt to a grid of resident CTAs in equal runs (lengths are read
+// on the device), so ragged batches and a single long sequence load every SM
+// alike; an item cut by a run's end leaves partial results that a second kernel
+// joins in order (the same result every time).
 //
 // Bound by HBM (a byte per cached element): a unit's K and V rows arrive by TMA
-// (swizzled to the head's row length).  Four warps a CTA; the nm warps that
-// share an item's units (one m-tile each) share 3 nm slots, a warp with an
-// m-tile of its own has three: its next two units are in flight while it
-// computes.  (With whole blocks and one ring for the CTA a warp's next tile
-// could only start when its last was done: 48 us instead of KV8_B64_US for 64
-// sequences of up to 4096 positions.)  e4m3 values are exact in fp16 and
-// Blackwell converts two per instruction, so the products run in fp16 with
-// fp32 accumulation:
+// (swizzled to the head's row length) in slots of their own for each group of
+// warps that shares units, which fill them themselves.  e4m3 values are exact in
+// fp16 and Blackwell converts two per instruction, so the products run in fp16
+// with fp32 accumulation:
 //   scores  a lane's 32 contiguous bytes of a key row (16-byte loads, no bank
 //           conflicts under the swizzle) feed eight MMAs: the order of the dims
 //           inside a dot product is free, the query's fragments take the same;
 //   output  ldmatrix.trans on byte pairs gives a lane two keys x two dims; one
-//           byte permute splits them into the even and the odd dim's operand.
+//           byte permute splits them into rows g (even dims) and g + 8 (odd) of
+//           the A operand.  P turns from the scores' layout by movmatrix.
 // The query rows are scaled by a power of two into fp16's range (exact for
 // bf16; fp32 queries are split into a high and a low fp16 part, two MMAs, and
 // so are their probabilities).  Softmax in fp32, online, with p = 2^(s - m + 14):
@@ -46,7 +46,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kKeys = 32;                       // keys per unit
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kDepth = 3;                       // slots per warp
 constexpr int kCtasMax = 512;
 constexpr float kPBias = 14.f;                  // p <= 2^14 in fp16
 
@@ -60,11 +59,13 @@ struct Kv8Attn {
   int batch, ntok, nh, nkv, max_seq, nblk;
   int group;      // nh / nkv
   unsigned magic; // ceil(2^32 / group): r / group = umulhi(r, magic) for group > 1
-  int nm;       // m-tiles of an item: 1, 2 or 4
+  int nt;       // 8-row tiles of a warp: 1 or 2
+  int nm;       // warps that share an item's rows: 1, 2 or 4
+  int irows;    // rows of an item: 8 nt nm
   int mgroups;  // items of a (sequence, kv head)
   float scale;
   void* out;    // [batch][ntok][nh][hd]
-  float* part;  // [2 * CTAs][16 nm][hd + 2]: rows of partial items, then m and l of each row
+  float* part;  // [2 * CTAs][irows][hd + 2]: rows of partial items, then m and l of each row
   int ctas;     // of the split kernel
   int* err;
 };
@@ -73,6 +74,7 @@ struct Kv8Attn {
 
 __device__ __forceinline__ int seq_len(const Kv8Attn& a, int b) {
   const int n = a.lens ? a.lens[b] : a.fixed_len;
+  if (n > a.max_seq) atomicOr(a.err, kErrCapacity);
   return n > a.max_seq || n < 0 ? 0 : n;
 }
 // Query token of row r of a kv head's rows (r < 2^20: the rounding of the magic
@@ -82,7 +84,7 @@ __device__ __forceinline__ int row_tok(const Kv8Attn& a, int r) {
 }
 // Units that an item's rows see (the last row sees the most).
 __device__ __forceinline__ int item_units(const Kv8Attn& a, int len, int mg) {
-  const int last = min(a.ntok * a.group, (mg + 1) * a.nm * 16) - 1;
+  const int last = min(a.ntok * a.group, (mg + 1) * a.irows) - 1;
   const int keys = max(0, len - a.ntok + 1 + row_tok(a, last));
   return (keys + kKeys - 1) / kKeys;
 }
@@ -95,6 +97,8 @@ __device__ __forceinline__ int entry_units(const Kv8Attn& a, int e) {
 }
 // Every thread of the CTA (128) takes entries [*e0, *e1) and gets the units
 // before them; returns all entries' units.
+// BAR: the barrier of these 128 threads.
+template <int BAR>
 __device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int* s_warp, int* before, int* e0, int* e1) {
   const int entries = a.batch * a.mgroups, per = (entries + kThreads - 1) / kThreads;
   *e0 = min(entries, tid * per);
@@ -108,7 +112,7 @@ __device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int* s_wa
     if ((tid & 31) >= o) inc += v;
   }
   if ((tid & 31) == 31) s_warp[tid >> 5] = inc;
-  __syncthreads();
+  asm volatile("bar.sync %0, 128;" ::"n"(BAR) : "memory");
   int base = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -139,6 +143,12 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* x, uint32_t b0
       "{%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of 16-bit values spread over the warp.
+__device__ __forceinline__ uint32_t turn8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -182,16 +192,20 @@ __device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
       make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-template <typename T, int HD>
+template <int HD, int NT>
 struct SplitSmem {
+  // slots per warp: with one row tile three CTAs fit an SM, with two (twice the
+  // accumulators) two
+  static constexpr int kDepth = NT == 1 ? 2 : 3;
+  static constexpr int kCtas = NT == 1 ? 3 : 2;
   static constexpr size_t kTile = (size_t)kKeys * HD;
   static constexpr size_t kSlot = 2 * kTile;
   // a warp's rows at an item's end, over its share of the slots (free then);
-  // rows 16 floats longer against conflicts
-  static constexpr int kRowF = HD + 16;
-  static constexpr size_t kShare = kDepth * kSlot > 16 * kRowF * 4 ? kDepth * kSlot : (16 * kRowF * 4 + 1023) / 1024 * 1024;
+  // rows 4 floats longer against conflicts
+  static constexpr int kRows = 8 * NT, kRowF = HD + 4;
+  static constexpr size_t kShare = kDepth * kSlot > (size_t)kRows * kRowF * 4 ? kDepth * kSlot : (kRows * kRowF * 4 + 1023) / 1024 * 1024;
   static constexpr size_t kML = kWarps * kShare;
-  static constexpr size_t kNan = kML + (size_t)kWarps * 16 * 2 * 4;  // per warp: first NaN position of each dim
+  static constexpr size_t kNan = kML + (size_t)kWarps * kRows * 2 * 4;  // per warp: first NaN position of each dim
   static constexpr size_t kBars = kNan + (size_t)kWarps * HD * 4;
   static constexpr size_t kInts = kBars + 2 * kWarps * kDepth * 8;
   static constexpr size_t kTotal = kInts + 16 * 4 + 1024;
@@ -251,13 +265,14 @@ __device__ __noinline__ bool prepare_edge(uint8_t* vt, int stale, bool look, int
   return __any_sync(0xffffffffu, any);
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads, 2)
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
     kv8_split_kernel(const Kv8Attn a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-  using SM = SplitSmem<T, HD>;
+  using SM = SplitSmem<HD, NT>;
   constexpr bool kWide = sizeof(T) == 4;  // fp32: two fp16 parts of q and of p
   constexpr int kTerms = kWide ? 2 : 1;
-  constexpr int kNt = kKeys / 8, kC = HD / 16;
+  constexpr int kMt = kKeys / 16, kC = HD / 16, kW = HD / 16;  // 16-key tiles; 16-dim chunks; words of a lane's key row
+  constexpr int kDepth = SM::kDepth, kRows = SM::kRows;
   extern __shared__ __align__(1024) uint8_t kv8_smem_raw[];
   uint8_t* smem = kv8_smem_raw + ((1024u - (smem_u32(kv8_smem_raw) & 1023u)) & 1023u);
   float* MLw = reinterpret_cast<float*>(smem + SM::kML);
@@ -276,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // this CTA's run of units
   int before, e0, e1;
-  const int total = scan_entries(a, tid, s_int + 4, &before, &e0, &e1);
+  const int total = scan_entries<1>(a, tid, s_int + 4, &before, &e0, &e1);
   const int run = run_units(a, total);
   const int u0 = (int)min((long long)blockIdx.x * run, (long long)total), u1 = min(total, u0 + run);
   if (u0 < u1)
@@ -288,22 +303,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       before += n;
     }
-  if (blockIdx.x == 0 && a.lens)
-    for (int b = tid; b < a.batch; b += kThreads)
-      if (a.lens[b] > a.max_seq) atomicOr(a.err, kErrCapacity);
   __syncthreads();
   if (u0 >= u1) return;
   UnitWalk w;
   w.seek(a, s_int[0], s_int[1]);
 
-  const int kw = kWarps / a.nm;            // warps that split the keys of an m-tile
+  const int kw = kWarps / a.nm;            // warps that split an item's keys
   const int mt = warp % a.nm, kg = warp / a.nm;
   const int gq = lane >> 2, tq = lane & 3;
   const int G = a.group, rows = a.ntok * G;
   const int mi = lane >> 3, mr = lane & 7;
   const float sl2 = a.scale * kLog2e;
-  // the slots of this warp's group (the nm warps of one kg), a ring; the warp
-  // of m-tile 0 fills them
+  // the slots of this warp's group (the nm warps of one kg), a ring; its first
+  // warp fills them
   const int slots = kDepth * a.nm, slot0 = kg * slots;
   uint8_t* ring = smem + (size_t)kg * a.nm * SM::kShare;
   int fill_s = 0, use_s = 0;
@@ -313,64 +325,76 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int u = u0; u < u1;) {
     const int n = min(w.nu - w.at, u1 - u);        // units of this item here
     const bool whole = n == w.nu;
-    const int m0 = (w.mg * a.nm + mt) * 16;        // the m-tile's first row
-    const bool two = m0 + 8 < rows;                // rows 8..15 exist
+    const int m0 = w.mg * a.irows + mt * kRows;    // this warp's first row
     const size_t head = (size_t)w.b * a.nkv + w.g;
     const float* ksp = a.ks + head * a.nblk;
     const float* vsp = a.vs + head * a.nblk;
     const int tile_row = (int)head * a.max_seq;
 
-    // units kg, kg + kw, ... of the n are this group's
-    int fill = kg;
-    auto fill_next = [&]() {
-      if (fill >= n) return;
-      if (!tc_wait_asleep(&empty[slot0 + fill_s], fill_ph ^ 1u)) atomicOr(a.err, kErrTimeout);
-      uint64_t* bar = &full[slot0 + fill_s];
-      uint8_t* st = ring + (size_t)fill_s * SM::kSlot;
-      const int row = tile_row + (w.at + fill) * kKeys;
-      mbar_arrive_expect_tx(bar, (uint32_t)SM::kSlot);
-      tma_load_2d(st, &kmap, 0, row, bar);
-      tma_load_2d(st + SM::kTile, &vmap, 0, row, bar);
-      fill += kw;
-      if (++fill_s == slots) {
-        fill_s = 0;
-        fill_ph ^= 1u;
+    // the query rows' and first scales' loads go out before the tiles' (behind
+    // them they took 6900 cycles): row gq of each tile, the lane's HD / 4 dims
+    constexpr int kV = Storage<T>::kVec, kQ = HD / 4 / kV;
+    uint4 raw[NT][kQ];
+#pragma unroll
+    for (int h = 0; h < NT; ++h) {
+      const int r = m0 + gq + 8 * h, t = row_tok(a, r);
+#pragma unroll
+      for (int j = 0; j < kQ; ++j) raw[h][j] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) {
+        const T* src = reinterpret_cast<const T*>(a.q) + (long long)w.b * a.q_seq_stride +
+                       (long long)t * a.q_tok_stride + (long long)(w.g * G + r - t * G) * HD + tq * (HD / 4);
+        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+#pragma unroll
+          for (int j = 0; j < kQ; ++j) raw[h][j] = __ldg(reinterpret_cast<const uint4*>(src) + j);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kQ; ++j) {
+            float f[kV];
+#pragma unroll
+            for (int i = 0; i < kV; ++i) f[i] = to_f(src[j * kV + i]);
+            raw[h][j] = pack16<T>(f);
+          }
+        }
       }
-    };
-    if (mt == 0 && lane == 0)
-      for (int i = 0; i < slots; ++i) fill_next();
+    }
     float ks_n = 0.f, vs_n = 0.f;
     if (kg < n) {
       ks_n = __ldg(ksp + (w.at + kg) * kKeys / kBlk);
       vs_n = __ldg(vsp + (w.at + kg) * kKeys / kBlk);
     }
+    // units kg, kg + kw, ... of the n are this group's.  At an item's start every
+    // slot is free: a lane each fills them
+    auto copy_unit = [&](int unit, int slot) {
+      uint64_t* bar = &full[slot0 + slot];
+      uint8_t* st = ring + (size_t)slot * SM::kSlot;
+      const int row = tile_row + (w.at + unit) * kKeys;
+      mbar_arrive_expect_tx(bar, (uint32_t)SM::kSlot);
+      tma_load_2d(st, &kmap, 0, row, bar);
+      tma_load_2d(st + SM::kTile, &vmap, 0, row, bar);
+    };
+    const int mine = (n - kg + kw - 1) / kw;       // this group's units
+    const int early = min(slots, mine);
+    if (mt == 0 && lane < early) {
+      int slot = fill_s + lane;
+      if (slot >= slots) slot -= slots;
+      copy_unit(kg + lane * kw, slot);
+    }
+    fill_s += early;
+    if (fill_s >= slots) {
+      fill_s -= slots;
+      fill_ph ^= 1u;
+    }
+    int fill = kg + early * kw;
 
-    // query fragments: rows gq and gq + 8, the lane's HD / 4 contiguous dims
-    uint32_t qa[kTerms][HD / 16][4];
-    float sc[2];
-    int lim[2];
+    // query fragments (the B operand: row gq, the lane's dims in words of four)
+    uint32_t qb[kTerms][NT][kW][2];
+    float sc[NT][2];   // of rows 2 tq and 2 tq + 1 of each tile, as the scores sit
+    int lim[NT][2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = m0 + gq + 8 * h;
+    for (int h = 0; h < NT; ++h) {
       float f[HD / 4];
-      lim[h] = 0;
-      if (r < rows) {
-        const int t = row_tok(a, r), hq = r - t * G;
-        lim[h] = w.len - a.ntok + 1 + t;
-        const T* src = reinterpret_cast<const T*>(a.q) + (long long)w.b * a.q_seq_stride +
-                       (long long)t * a.q_tok_stride + (long long)(w.g * G + hq) * HD + tq * (HD / 4);
-        if ((reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-          constexpr int kV = Storage<T>::kVec;
 #pragma unroll
-          for (int j = 0; j < HD / 4 / kV; ++j) unpack16<T>(__ldg(reinterpret_cast<const uint4*>(src) + j), f + j * kV);
-        } else {
-#pragma unroll
-          for (int j = 0; j < HD / 4; ++j) f[j] = to_f(src[j]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < HD / 4; ++j) f[j] = 0.f;
-      }
+      for (int j = 0; j < kQ; ++j) unpack16<T>(raw[h][j], f + j * kV);
       float m = 0.f;
 #pragma unroll
       for (int j = 0; j < HD / 4; ++j) m = fmaxf(m, fabsf(f[j]));
@@ -379,29 +403,38 @@ __global__ void __launch_bounds__(kThreads, 2)
       // 2^k brings the row's largest magnitude to [256, 512)
       const int k = m > 0.f ? min(126, 127 + 8 - (int)(__float_as_uint(m) >> 23)) : 0;
       const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-      sc[h] = sl2 * __uint_as_float((uint32_t)(127 - k) << 23);
+      const float down = sl2 * __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll
-      for (int j = 0; j < HD / 16; ++j) {
+      for (int j = 0; j < kW; ++j) {
         const float x0 = f[4 * j] * up, x1 = f[4 * j + 1] * up, x2 = f[4 * j + 2] * up, x3 = f[4 * j + 3] * up;
-        qa[0][j][h] = pack_f16x2(x0, x1);
-        qa[0][j][2 + h] = pack_f16x2(x2, x3);
+        qb[0][h][j][0] = pack_f16x2(x0, x1);
+        qb[0][h][j][1] = pack_f16x2(x2, x3);
         if constexpr (kWide) {
-          const float2 y0 = unpack_f16x2(qa[0][j][h]), y1 = unpack_f16x2(qa[0][j][2 + h]);
-          qa[1][j][h] = pack_f16x2(x0 - y0.x, x1 - y0.y);
-          qa[1][j][2 + h] = pack_f16x2(x2 - y1.x, x3 - y1.y);
+          const float2 y0 = unpack_f16x2(qb[0][h][j][0]), y1 = unpack_f16x2(qb[0][h][j][1]);
+          qb[1][h][j][0] = pack_f16x2(x0 - y0.x, x1 - y0.y);
+          qb[1][h][j][1] = pack_f16x2(x2 - y1.x, x3 - y1.y);
         }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        sc[h][j] = __shfl_sync(0xffffffffu, down, 4 * (2 * tq + j));
+        const int r = m0 + 8 * h + 2 * tq + j;
+        lim[h][j] = r < rows ? w.len - a.ntok + 1 + row_tok(a, r) : 0;
       }
     }
     // keys below every row's limit need no mask
     const int clear = w.len - a.ntok + 1 + row_tok(a, min(m0, rows - 1));
     bool some_nan = false;  // first_nan is in use
 
-    float o[kC][8];  // per chunk of 16 dims: even dims' tile, odd dims' tile
+    float o[NT][kC][4];  // (dim 16 c + 2 gq, row 2 tq), (same, + 1), (dim + 1, row), (dim + 1, row + 1)
+    float m_run[NT][2], l_run[NT][2];
 #pragma unroll
-    for (int c = 0; c < kC; ++c)
+    for (int h = 0; h < NT; ++h) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[c][j] = 0.f;
-    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+      for (int c = 0; c < kC; ++c) o[h][c][0] = o[h][c][1] = o[h][c][2] = o[h][c][3] = 0.f;
+      m_run[h][0] = m_run[h][1] = -INFINITY;
+      l_run[h][0] = l_run[h][1] = 0.f;
+    }
     float unit = 0.f, unit_max = 0.f;
 
     for (int x = kg; x < n; x += kw) {
@@ -414,31 +447,39 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!tc_wait_asleep(&full[slot0 + use_s], use_ph) && lane == 0) atomicOr(a.err, kErrTimeout);
       uint8_t* tile = ring + (size_t)use_s * SM::kSlot;
       const uint32_t kt = smem_u32(tile), vt = kt + (uint32_t)SM::kTile;
-      if (m0 < rows) {  // (three m-tiles of four: the last has no rows)
-        // ---- scores: four key tiles side by side, so that no MMA waits for the last
-        float s[kNt][4];
-        uint32_t kb[kNt][HD / 16];
+      if (m0 < rows) {  // (three warps' rows of four: the last has none)
+        // ---- scores: the key tiles side by side, so that no MMA waits for the last
+        float s[NT][kMt][4];
+        uint32_t kb[kMt][2][kW];
 #pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-          const int r = nt * 8 + gq;
-          if constexpr (HD == 128) {
-            lds_words<16>(kt + tile_off<HD>(r, 2 * tq), kb[nt]);
-            lds_words<16>(kt + tile_off<HD>(r, 2 * tq + 1), kb[nt] + 4);
-          } else if constexpr (HD == 64) {
-            lds_words<16>(kt + tile_off<HD>(r, tq), kb[nt]);
-          } else {
-            lds_words<8>(kt + tile_off<HD>(r, tq >> 1) + 8 * (tq & 1), kb[nt]);
+        for (int m = 0; m < kMt; ++m)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 16 * m + 8 * i + gq;
+            if constexpr (HD == 128) {
+              lds_words<16>(kt + tile_off<HD>(r, 2 * tq), kb[m][i]);
+              lds_words<16>(kt + tile_off<HD>(r, 2 * tq + 1), kb[m][i] + 4);
+            } else if constexpr (HD == 64) {
+              lds_words<16>(kt + tile_off<HD>(r, tq), kb[m][i]);
+            } else {
+              lds_words<8>(kt + tile_off<HD>(r, tq >> 1) + 8 * (tq & 1), kb[m][i]);
+            }
           }
-        }
 #pragma unroll
-        for (int j = 0; j < HD / 16; ++j)
+        for (int h = 0; h < NT; ++h)
 #pragma unroll
-          for (int nt = 0; nt < kNt; ++nt) {
-            const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(kb[nt][j] & 0xffffu));
-            const uint32_t b1 = e4m3x2_to_f16x2((uint16_t)(kb[nt][j] >> 16));
-            mma_f16(s[nt], qa[0][j], b0, b1);
-            if constexpr (kWide) mma_f16(s[nt], qa[1][j], b0, b1);
+          for (int m = 0; m < kMt; ++m) s[h][m][0] = s[h][m][1] = s[h][m][2] = s[h][m][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kW; ++j)
+#pragma unroll
+          for (int m = 0; m < kMt; ++m) {
+            const uint32_t ka[4] = {
+                e4m3x2_to_f16x2((uint16_t)(kb[m][0][j] & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(kb[m][1][j] & 0xffffu)),
+                e4m3x2_to_f16x2((uint16_t)(kb[m][0][j] >> 16)), e4m3x2_to_f16x2((uint16_t)(kb[m][1][j] >> 16))};
+#pragma unroll
+            for (int h = 0; h < NT; ++h)
+#pragma unroll
+              for (int e = 0; e < kTerms; ++e) mma_f16(s[h][m], ka, qb[e][h][j][0], qb[e][h][j][1]);
           }
         // ---- the unit of this block's V scale (never 2^60 below the largest so
         // far: the output in units of it stays in range)
@@ -447,71 +488,72 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float ratio = unit_new == unit ? 1.f : unit / unit_new;
         const float pf = vsc == unit_new ? 1.f : vsc / unit_new;
         unit = unit_new;
-        // ---- softmax of rows gq (h = 0) and gq + 8 (h = 1)
+        // ---- softmax: value 2 i + j of tile m is key 16 m + 8 i + gq, row 2 tq + j
         const bool edge = key0 + kKeys > clear;
-        uint32_t pa[kTerms][kNt / 2][4];
-        float move[2] = {ratio, ratio};  // of the output: to the new maximum and unit
+        uint32_t pb[kTerms][NT][kMt][2];
+        float move[NT][2];  // of the output: to the new maximum and unit
+        bool moved = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h == 1 && !two) {
+        for (int h = 0; h < NT; ++h) {
 #pragma unroll
-            for (int e = 0; e < kTerms; ++e)
+          for (int j = 0; j < 2; ++j) {
+            const float f = sc[h][j] * ksc;
+            float mx = -INFINITY;
 #pragma unroll
-              for (int kk = 0; kk < kNt / 2; ++kk) pa[e][kk][1] = pa[e][kk][3] = 0u;
-            continue;
+            for (int m = 0; m < kMt; ++m)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                float v = s[h][m][2 * i + j] * f;
+                if (edge && key0 + 16 * m + 8 * i + gq >= lim[h][j]) v = -INFINITY;
+                s[h][m][2 * i + j] = v;
+                mx = fmaxf(mx, v);
+              }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = fmaxf(m_run[h][j], mx);
+            const float ms = mn == -INFINITY ? 0.f : mn;
+            const float alpha = ex2(m_run[h][j] - ms);
+            move[h][j] = ratio * alpha;
+            moved |= move[h][j] != 1.f;
+            m_run[h][j] = mn;
+            float sum = 0.f;
+#pragma unroll
+            for (int m = 0; m < kMt; ++m)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float p = ex2(s[h][m][2 * i + j] - ms + kPBias);
+                s[h][m][2 * i + j] = p;
+                sum += p;
+              }
+            l_run[h][j] = l_run[h][j] * alpha + sum;
           }
-          const float f = sc[h] * ksc;
-          float mx = -INFINITY;
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float v = s[nt][2 * h + j] * f;
-              if (edge && key0 + nt * 8 + 2 * tq + j >= lim[h]) v = -INFINITY;
-              s[nt][2 * h + j] = v;
-              mx = fmaxf(mx, v);
-            }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m_run[h], mx);
-          const float ms = mn == -INFINITY ? 0.f : mn;
-          const float alpha = ex2(m_run[h] - ms);
-          move[h] *= alpha;
-          m_run[h] = mn;
-          float sum = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float p = ex2(s[nt][2 * h + j] - ms + kPBias);
-              s[nt][2 * h + j] = p;
-              sum += p;
-            }
-          l_run[h] = l_run[h] * alpha + sum;
           if (pf != 1.f) {
 #pragma unroll
-            for (int nt = 0; nt < kNt; ++nt) {
-              s[nt][2 * h] *= pf;
-              s[nt][2 * h + 1] *= pf;
-            }
+            for (int m = 0; m < kMt; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[h][m][i] *= pf;
           }
 #pragma unroll
-          for (int kk = 0; kk < kNt / 2; ++kk)
+          for (int m = 0; m < kMt; ++m)
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const float p0 = s[2 * kk + v][2 * h], p1 = s[2 * kk + v][2 * h + 1];
-              pa[0][kk][2 * v + h] = pack_f16x2(p0, p1);
+            for (int i = 0; i < 2; ++i) {
+              const float p0 = s[h][m][2 * i], p1 = s[h][m][2 * i + 1];
+              const uint32_t hi = pack_f16x2(p0, p1);
+              pb[0][h][m][i] = turn8x8(hi);
               if constexpr (kWide) {
-                const float2 hi = unpack_f16x2(pa[0][kk][2 * v + h]);
-                pa[1][kk][2 * v + h] = pack_f16x2(p0 - hi.x, p1 - hi.y);
+                const float2 y = unpack_f16x2(hi);
+                pb[1][h][m][i] = turn8x8(pack_f16x2(p0 - y.x, p1 - y.y));
               }
             }
         }
-        if (__any_sync(0xffffffffu, move[0] != 1.f || move[1] != 1.f)) {
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int c = 0; c < kC; ++c)
+          for (int h = 0; h < NT; ++h)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[c][j] *= move[(j >> 1) & 1];
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[h][c][j] *= move[h][j & 1];
         }
         // ---- rows past the sequence, NaN that not every row sees
         bool drop_nan = false;
@@ -526,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         // ---- output
 #pragma unroll
-        for (int kk = 0; kk < kNt / 2; ++kk) {
+        for (int kk = 0; kk < kMt; ++kk) {
           uint32_t r[kC / 2][4];
 #pragma unroll
           for (int c2 = 0; c2 < kC / 2; ++c2)
@@ -542,14 +584,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             // bytes (key, dim): (0, even), (0, odd), (1, even), (1, odd)
             const uint32_t y0 = __byte_perm(r[c / 2][2 * (c & 1)], 0u, 0x3120);
             const uint32_t y1 = __byte_perm(r[c / 2][2 * (c & 1) + 1], 0u, 0x3120);
-            const uint32_t e0v = e4m3x2_to_f16x2((uint16_t)(y0 & 0xffffu)), e1v = e4m3x2_to_f16x2((uint16_t)(y1 & 0xffffu));
-            const uint32_t d0v = e4m3x2_to_f16x2((uint16_t)(y0 >> 16)), d1v = e4m3x2_to_f16x2((uint16_t)(y1 >> 16));
-            mma_f16(o[c], pa[0][kk], e0v, e1v);
-            mma_f16(o[c] + 4, pa[0][kk], d0v, d1v);
-            if constexpr (kWide) {
-              mma_f16(o[c], pa[1][kk], e0v, e1v);
-              mma_f16(o[c] + 4, pa[1][kk], d0v, d1v);
-            }
+            const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)(y0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(y0 >> 16)),
+                                    e4m3x2_to_f16x2((uint16_t)(y1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(y1 >> 16))};
+#pragma unroll
+            for (int h = 0; h < NT; ++h)
+#pragma unroll
+              for (int e = 0; e < kTerms; ++e) mma_f16(o[h][c], va, pb[e][h][kk][0], pb[e][h][kk][1]);
           }
         }
         if (edge) fence_async_smem();  // zeroed rows before the slot's next copy
@@ -557,9 +597,19 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&empty[slot0 + use_s]);
-        if (mt == 0) fill_next();
+        if (mt == 0 && fill < n) {
+          if (!tc_wait_asleep(&empty[slot0 + fill_s], fill_ph ^ 1u)) atomicOr(a.err, kErrTimeout);
+          copy_unit(fill, fill_s);
+        }
       }
       __syncwarp();
+      if (fill < n) {
+        fill += kw;
+        if (++fill_s == slots) {
+          fill_s = 0;
+          fill_ph ^= 1u;
+        }
+      }
       if (++use_s == slots) {
         use_s = 0;
         use_ph ^= 1u;
@@ -567,70 +617,79 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     // ---- the item's rows: each warp's normalised output, maximum and sum, over
-    // its share of the slots (all consumed: its group's, once every warp is here)
+    // its share of the slots (all consumed, once every warp is here)
     asm volatile("bar.sync 1, 128;" ::: "memory");
     float* Ow = reinterpret_cast<float*>(smem + (size_t)warp * SM::kShare);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float l = l_run[h];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int r = gq + 8 * h;
-      if (some_nan) {
+    for (int h = 0; h < NT; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float l = l_run[h][j];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int r = 8 * h + 2 * tq + j;
+        if (some_nan) {
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+              if (first_nan[16 * c + 2 * gq + d] < lim[h][j]) o[h][c][2 * d + j] = NAN;
+        }
 #pragma unroll
         for (int c = 0; c < kC; ++c)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (first_nan[16 * c + 4 * tq + j] < lim[h]) o[c][2 * h + (j >> 1) + 4 * (j & 1)] = NAN;
+          *reinterpret_cast<float2*>(Ow + r * SM::kRowF + 16 * c + 2 * gq) =
+              make_float2(o[h][c][j] * inv * unit, o[h][c][2 + j] * inv * unit);
+        if (gq == 0) {
+          MLw[2 * (kRows * warp + r)] = m_run[h][j];
+          MLw[2 * (kRows * warp + r) + 1] = l;
+        }
       }
-#pragma unroll
-      for (int c = 0; c < kC; ++c)
-        *reinterpret_cast<float4*>(Ow + r * SM::kRowF + 16 * c + 4 * tq) =
-            make_float4(o[c][2 * h] * inv * unit, o[c][4 + 2 * h] * inv * unit, o[c][2 * h + 1] * inv * unit,
-                        o[c][5 + 2 * h] * inv * unit);
-      if (tq == 0) {
-        MLw[2 * (16 * warp + r)] = m_run[h];
-        MLw[2 * (16 * warp + r) + 1] = l;
-      }
-    }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     // ---- joined over the key-splitting warps: to the output, or to this CTA's
     // first (slot 0: the item began at or before the run) or last partial
     const int part = 2 * blockIdx.x + (u != u0 ? 1 : 0);
-    const int irows = 16 * a.nm, here = min(irows, rows - w.mg * irows);
-    for (int j = tid; j < here * (HD / 4); j += kThreads) {
-      const int rr = j / (HD / 4), d = j % (HD / 4) * 4;  // row rr % 16 of warp rr / 16; the next key part is nm warps on
+    const int here = min(a.irows, rows - w.mg * a.irows);
+    for (int i = tid; i < here * (HD / 4); i += kThreads) {
+      const int rr = i / (HD / 4), d = i % (HD / 4) * 4;
+      // row rr % kRows of warp rr / kRows; the next key part is nm warps on
+      float2 ml[kWarps];
+      float4 v[kWarps];
       float M = -INFINITY;
-      for (int k = 0; k < kw; ++k) M = fmaxf(M, MLw[2 * (rr + 16 * a.nm * k)]);
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        if (k < kw) {
+          const int wp = rr / kRows + k * a.nm, lr = rr % kRows;
+          ml[k] = *reinterpret_cast<const float2*>(MLw + 2 * (kRows * wp + lr));
+          v[k] = *reinterpret_cast<const float4*>(smem + (size_t)wp * SM::kShare + (lr * SM::kRowF + d) * 4);
+          M = fmaxf(M, ml[k].x);
+        }
       const float ms = M == -INFINITY ? 0.f : M;
       float W = 0.f;
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < kw; ++k) {
-        const int at = rr + 16 * a.nm * k;
-        const float l = MLw[2 * at + 1];
-        if (l == 0.f) continue;
-        const float e = l * ex2(MLw[2 * at] - ms);
-        const float4 v = *reinterpret_cast<const float4*>(
-            smem + (size_t)(at >> 4) * SM::kShare + ((at & 15) * SM::kRowF + d) * 4);
-        W += e;
-        y.x = fmaf(e, v.x, y.x);
-        y.y = fmaf(e, v.y, y.y);
-        y.z = fmaf(e, v.z, y.z);
-        y.w = fmaf(e, v.w, y.w);
-      }
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        if (k < kw && ml[k].y != 0.f) {
+          const float e = ml[k].y * ex2(ml[k].x - ms);
+          W += e;
+          y.x = fmaf(e, v[k].x, y.x);
+          y.y = fmaf(e, v[k].y, y.y);
+          y.z = fmaf(e, v[k].z, y.z);
+          y.w = fmaf(e, v[k].w, y.w);
+        }
       const float inv = W == 0.f ? 0.f : 1.f / W;
       y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       if (whole) {
-        const int r = w.mg * irows + rr, t = row_tok(a, r);
+        const int r = w.mg * a.irows + rr, t = row_tok(a, r);
         store_row4(reinterpret_cast<T*>(a.out) +
                        (((size_t)w.b * a.ntok + t) * a.nh + w.g * G + (r - t * G)) * HD + d,
                    y);
       } else {
-        const size_t at = (size_t)part * irows + rr;
+        const size_t at = (size_t)part * a.irows + rr;
         *reinterpret_cast<float4*>(a.part + at * HD + d) = y;
         if (d == 0)
-          *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * irows * HD + 2 * at) = make_float2(M, W);
+          *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * a.irows * HD + 2 * at) = make_float2(M, W);
       }
     }
     u += n;
@@ -644,29 +703,38 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Joins the partial rows of the items that a run's end cut, in the runs' order,
-// and zeroes the rows of items without a visible key.  One CTA per row.
+// and zeroes the rows of items without a visible key.  One CTA per row: a long
+// sequence alone on the machine has a partial row from every CTA of the split
+// kernel, so eight groups of lanes (head dim 128) read them, eight loads in
+// flight each.
+constexpr int kJoinThreads = 256;
 template <typename T, int HD>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const Kv8Attn a) {
-  constexpr int kLanes = HD / 4, kGroups = 128 / kLanes;
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a) {
+  constexpr int kLanes = HD / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
   constexpr int kMost = kCtasMax;  // an item's partial rows: at most one per CTA of the split kernel
   __shared__ float s_w[kMost], s_m[kMost];
   __shared__ int s_int[8];
   __shared__ float s_red[8];
-  __shared__ float4 s_o[128];
+  __shared__ float4 s_o[kJoinThreads];
   pdl_launch_dependents();
   const int r = blockIdx.x, g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int irows = 16 * a.nm, mg = r / irows, rr = r - mg * irows;
-  const int G = a.group, t = row_tok(a, r);
+  const int irows = a.irows, mg = r / irows, rr = r - mg * irows;
+  const int t = row_tok(a, r);
   const int e = b * a.mgroups + mg;
-  int before, e0, e1;
+  int before = 0, e0 = 0, e1 = 0;
   pdl_wait();
-  const int total = scan_entries(a, tid, s_int, &before, &e0, &e1);
-  if (e0 <= e && e < e1) {
-    for (int x = e0; x < e; ++x) before += entry_units(a, x);
-    s_int[4] = before;
+  int total = 0;
+  if (tid < kThreads) {
+    total = scan_entries<1>(a, tid, s_int, &before, &e0, &e1);
+    if (e0 <= e && e < e1) {
+      for (int x = e0; x < e; ++x) before += entry_units(a, x);
+      s_int[4] = before;
+      s_int[5] = total;
+    }
   }
   __syncthreads();
-  T* out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.ntok + t) * a.nh + g * G + (r - t * G)) * HD;
+  total = s_int[5];
+  T* out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.ntok + t) * a.nh + g * a.group + (r - t * a.group)) * HD;
   const int nu = item_units(a, seq_len(a, b), mg);
   const int lane = tid % kLanes, grp = tid / kLanes;
   if (nu == 0) {
@@ -676,89 +744,109 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const Kv8Attn a) {
   const int run = run_units(a, total), us = s_int[4] + g * nu;
   const int c0 = us / run, n = (us + nu - 1) / run - c0 + 1;
   if (n == 1) return;  // the split kernel has written it
+  // partial row i: of CTA c0 + i, its first partial unless the item began inside its run
+  const size_t at0 = ((size_t)2 * c0 + (us > c0 * run ? 1 : 0)) * irows + rr;
+  const size_t at1 = (size_t)2 * c0 * irows + rr, step = (size_t)2 * irows;
   const float* ml = a.part + (size_t)2 * a.ctas * irows * HD;
-  auto row_of = [&](int i) { return (size_t)(2 * (c0 + i) + (us > (c0 + i) * run ? 1 : 0)) * irows + rr; };
   float M = -INFINITY;
-  for (int i = tid; i < n; i += 128) {
-    const float2 v = *reinterpret_cast<const float2*>(ml + 2 * row_of(i));
+  for (int i = tid; i < n; i += kJoinThreads) {
+    const float2 v = *reinterpret_cast<const float2*>(ml + 2 * (i == 0 ? at0 : at1 + i * step));
     s_m[i] = v.x;
     s_w[i] = v.y;
     M = fmaxf(M, v.x);
   }
+  // the first loads of the rows do not wait for the weights
+  float4 v[kBatch];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kGroups;
+      v[k] = i < n ? *reinterpret_cast<const float4*>(a.part + (i == 0 ? at0 : at1 + i * step) * HD + 4 * lane)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  load(grp);
   M = warp_max(M);
   if ((tid & 31) == 0) s_red[tid >> 5] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+#pragma unroll
+  for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, s_red[k]);
   const float ms = M == -INFINITY ? 0.f : M;
-  float W = 0.f;
-  for (int i = tid; i < n; i += 128) {
-    const float x = s_w[i] == 0.f ? 0.f : s_w[i] * ex2(s_m[i] - ms);
-    s_w[i] = x;
-    W += x;
-  }
-  W = warp_sum(W);
-  if ((tid & 31) == 0) s_red[4 + (tid >> 5)] = W;
+  for (int i = tid; i < n; i += kJoinThreads) s_w[i] = s_w[i] == 0.f ? 0.f : s_w[i] * ex2(s_m[i] - ms);
   __syncthreads();
-  W = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = grp; i < n; i += kGroups) {
-    const float x = s_w[i];
-    if (x == 0.f) continue;
-    const float4 v = *reinterpret_cast<const float4*>(a.part + row_of(i) * HD + 4 * lane);
-    y.x = fmaf(x, v.x, y.x);
-    y.y = fmaf(x, v.y, y.y);
-    y.z = fmaf(x, v.z, y.z);
-    y.w = fmaf(x, v.w, y.w);
+  float W = 0.f;
+  for (int i0 = grp; i0 < n; i0 += kBatch * kGroups) {
+    if (i0 != grp) load(i0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + k * kGroups;
+      const float x = i < n ? s_w[i] : 0.f;
+      if (x == 0.f) continue;  // (a row that saw no key there; NaN is kept)
+      W += x;
+      y.x = fmaf(x, v[k].x, y.x);
+      y.y = fmaf(x, v[k].y, y.y);
+      y.z = fmaf(x, v[k].z, y.z);
+      y.w = fmaf(x, v[k].w, y.w);
+    }
   }
   s_o[tid] = y;
+  if (lane == 0) s_m[grp] = W;  // (s_m is read no more)
   __syncthreads();
   if (grp == 0) {
     for (int k = 1; k < kGroups; ++k) {
-      const float4 v = s_o[k * kLanes + lane];
-      y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+      const float4 u = s_o[k * kLanes + lane];
+      y = make_float4(y.x + u.x, y.y + u.y, y.z + u.z, y.w + u.w);
+      W += s_m[k];
     }
     const float inv = W == 0.f ? 0.f : 1.f / W;
     store_row4(out + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
   }
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int NT>
 q2_status split_t(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaStream_t st) {
-  using SM = SplitSmem<T, HD>;
-  auto* kernel = kv8_split_kernel<T, HD>;
+  using SM = SplitSmem<HD, NT>;
+  auto* kernel = kv8_split_kernel<T, HD, NT>;
   Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.batch * a.nkv * a.max_seq;
   Q2_TRY(make_tmap_2d_u8(&km, kc, rows, HD, HD, kKeys, HD, HD));
   Q2_TRY(make_tmap_2d_u8(&vm, vc, rows, HD, HD, kKeys, HD, HD));
   Q2_LAUNCH(kernel, dim3(a.ctas), dim3(kThreads), SM::kTotal, st, true, a, km, vm);
-  Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(a.ntok * a.group, a.nkv, a.batch), dim3(128), 0, st, true, a);
+  Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(a.ntok * a.group, a.nkv, a.batch), dim3(kJoinThreads), 0, st, true, a);
   return Q2_OK;
 }
 
 template <typename T>
 q2_status split(const Kv8Attn& a, int hd, const uint8_t* kc, const uint8_t* vc, cudaStream_t st) {
-  switch (hd) {
-    case 32: return split_t<T, 32>(a, kc, vc, st);
-    case 64: return split_t<T, 64>(a, kc, vc, st);
-    default: return split_t<T, 128>(a, kc, vc, st);
+  switch (2 * hd + a.nt) {
+    case 65: return split_t<T, 32, 1>(a, kc, vc, st);
+    case 66: return split_t<T, 32, 2>(a, kc, vc, st);
+    case 129: return split_t<T, 64, 1>(a, kc, vc, st);
+    case 130: return split_t<T, 64, 2>(a, kc, vc, st);
+    case 257: return split_t<T, 128, 1>(a, kc, vc, st);
+    default: return split_t<T, 128, 2>(a, kc, vc, st);
   }
 }
 
-// m-tiles per item, items per kv head, CTAs and workspace of the split kernel.
+// Row tiles per warp, warps per item, items per kv head, CTAs and workspace of
+// the split kernel.
 struct SplitPlan {
-  int nm, mgroups, ctas;
+  int nt, nm, irows, mgroups, ctas;
   size_t bytes;
 };
 SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd) {
   SplitPlan p;
-  const int mtiles = ceil_div((long long)(ntok * (nh / nkv)), 16);
-  p.nm = mtiles > 2 ? 4 : mtiles;
-  p.mgroups = ceil_div(mtiles, p.nm);
-  p.ctas = num_sms() * 2;  // all resident at once
+  const int rows = (int)(ntok * (nh / nkv));
+  p.nt = rows > 8 ? 2 : 1;
+  const int warps = ceil_div(rows, 8 * p.nt);
+  p.nm = warps > 2 ? 4 : warps;
+  p.irows = 8 * p.nt * p.nm;
+  p.mgroups = ceil_div(rows, p.irows);
+  p.ctas = num_sms() * (p.nt == 1 ? 3 : 2);  // all resident at once
   if (p.ctas > kCtasMax) p.ctas = kCtasMax;
-  p.bytes = (size_t)2 * p.ctas * 16 * p.nm * (hd + 2) * sizeof(float);
+  p.bytes = (size_t)2 * p.ctas * p.irows * (hd + 2) * sizeof(float);
   return p;
 }
 
@@ -776,7 +864,9 @@ q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, voi
   }
   a.group = a.nh / a.nkv;
   a.magic = a.group == 1 ? 0u : (unsigned)(((1ull << 32) + a.group - 1) / a.group);
+  a.nt = p.nt;
   a.nm = p.nm;
+  a.irows = p.irows;
   a.mgroups = p.mgroups;
   a.ctas = p.ctas;
   a.part = static_cast<float*>(ws);
