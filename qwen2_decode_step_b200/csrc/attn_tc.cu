@@ -201,7 +201,15 @@ struct AttnTc {
   int ts;        // the later items' key ranges (CTA n_whole + p: range p / n_tail of item n_whole + p % n_tail)
   float* part;   // [n_tail * ts] slots of kSlotFloats
   int* cnt;      // [n_tail] ranges done (0 between launches)
+  const int* vnan;  // null, or [nkv][hd]: INT32_MAX - the first position with a NaN of V in that dim (0: none)
 };
+
+// Eight dims of the row at position pos: NaN where one of V's lies at or before it.
+__device__ __forceinline__ void mark_nan(const int* vnan, int pos, float* f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (INT32_MAX - __ldg(vnan + i) <= pos) f[i] = NAN;
+}
 
 // A slot: O (fp32, [row][dim]), then m and l of each row.
 constexpr int kSlotFloats = kQB * kHD + 2 * kQB;
@@ -474,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float f[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(ov[e + t]) * inv;
+            if (a.vnan) mark_nan(a.vnan + (size_t)kvh * kHD + cb + 32 * c + e, a.pos0 + row, f);
             *reinterpret_cast<uint4*>(out + 32 * c + e) = pack16<bf16>(f);
           }
         }
@@ -534,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float f[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) f[u] = o[e + u] * inv;
+            if (a.vnan) mark_nan(a.vnan + (size_t)kvh * kHD + cb + e, a.pos0 + row, f);
             *reinterpret_cast<uint4*>(out + e) = pack16<bf16>(f);
           }
         }
@@ -569,6 +579,13 @@ static const bf16* seq_v(const AttnRows& a) {
 constexpr int kMaxTs = 6;
 constexpr size_t kCntBytes = 4096;
 size_t attn_tc_ws_bytes() { return kCntBytes + (size_t)num_sms() * kMaxTs * kSlotFloats * sizeof(float); }
+
+size_t attn_tc_ws_need(int rows, int pos0, int nh) {
+  int n_whole = 0, ts = 1;
+  attn_tc_plan(rows, pos0, nh, num_sms(), true, &n_whole, &ts);
+  const size_t tail = (size_t)((rows + kQB - 1) / kQB) * nh - n_whole;
+  return kCntBytes + (ts > 1 ? tail * ts * kSlotFloats * sizeof(float) : 0);
+}
 
 int attn_tc_slot_capacity(int sms) { return sms * kMaxTs; }
 int attn_tc_counter_capacity() { return (int)(kCntBytes / sizeof(int)); }
@@ -613,7 +630,7 @@ bool attn_tc_supported(const AttnRows& a, int dtype) {
          (reinterpret_cast<uintptr_t>(seq_v(a)) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 }
 
-q2_status launch_attn_tc(const AttnRows& a, void* ws, int* err, cudaStream_t st) {
+q2_status launch_attn_tc(const AttnRows& a, void* ws, int* err, cudaStream_t st, const int* vnan) {
   if (a.rows == 0) return Q2_OK;
   const int pos0 = a.base - 1;
   const long long keys = (long long)pos0 + a.rows;  // keys visible to the last row
@@ -647,6 +664,7 @@ q2_status launch_attn_tc(const AttnRows& a, void* ws, int* err, cudaStream_t st)
   p.out = a.out;
   p.out_row_stride = a.out_row_stride;
   p.err = err;
+  p.vnan = vnan;
   p.ntq = (a.rows + kQB - 1) / kQB;
   const int items = p.ntq * a.nh;
   attn_tc_plan(a.rows, pos0, a.nh, num_sms(), ws != nullptr, &p.n_whole, &p.ts);

@@ -31,8 +31,17 @@
 // largest at fp16's full 11 bits.  The scale of K multiplies the scores; the
 // output is accumulated in units of the current block's V scale and moved to
 // the next block's where that differs (a power of two: exact).
+//
+// Prompt rows (bf16, head dim 128, 512 rows of a kv head or more): the cache's K and
+// V are read back to bf16 (exact) in the workspace and the prompt attention on
+// tcgen05 runs over them.  That product is bound by the tensor core: the copy
+// moves 6 bytes per cached element once, against 4 rows x heads operations per
+// element (4096 rows over 32768 keys: 12 us of copy, 919 of attention).  A NaN of
+// V, which the zero probabilities of rows that do not see it would spread, is
+// taken out of the copy and put into the rows that do see it at the end.
 #include "common.cuh"
 #include "e4m3.cuh"
+#include "kernels.h"
 #include "kv8.h"
 #include "tcgen05.cuh"
 #include "tma.h"
@@ -850,14 +859,85 @@ SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd) {
   return p;
 }
 
+q2_status check_workspace(const void* ws, size_t have, size_t need) {
+  if (ws && !(reinterpret_cast<uintptr_t>(ws) & 255) && have >= need) return Q2_OK;
+  set_error("kv8 attention: the workspace is NULL, not 256-byte aligned or smaller than "
+            "q2_kv8_attention_workspace says");
+  return Q2_ERR_INVALID_ARG;
+}
+
+// ------------------------------------------------------------------ prompt rows
+
+// The tcgen05 attention takes 128 rows of one query head a tile, whether they
+// exist or not, and the copy of K and V comes before it; the split kernel's time
+// goes with the rows of a kv head.  12 / 2 heads over 32768 keys: 64 prompt
+// tokens (384 rows) 100 us here against 115 there, 128 (768 rows) 176 against
+// 115; over 4096 keys 128 tokens 52 against 62, 4 / 4 heads 64 tokens 25 against 62.
+constexpr int kTcRows = 512;
+bool use_tc(size_t ntok, size_t group, size_t hd, int dtype) {
+  return dtype == Q2_BF16 && hd == 128 && ntok >= 16 && ntok * group >= kTcRows;
+}
+
+// Workspace: the tcgen05 attention's counters and, next to them, the NaN words
+// (one memset clears both), its slots, K, V.
+struct TcPlan {
+  size_t nan, k, v, bytes;
+};
+TcPlan tc_plan(size_t rows, size_t total, size_t nh, size_t nkv) {
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  TcPlan p;
+  const size_t cache = up(total * nkv * 128 * 2);
+  p.nan = up(attn_tc_ws_need((int)rows, (int)(total - rows), (int)nh));
+  p.k = p.nan + up(nkv * 128 * sizeof(int));
+  p.v = p.k + cache;
+  p.bytes = p.v + cache;
+  return p;
+}
+
+q2_status attn_tc(const Kv8Attn& a, const void* kc, const void* vc, void* ws, size_t ws_bytes, cudaStream_t st) {
+  const TcPlan p = tc_plan(a.ntok, a.fixed_len, a.nh, a.nkv);
+  Q2_TRY(check_workspace(ws, ws_bytes, p.bytes));
+  char* base = static_cast<char*>(ws);
+  Q2_CUDA_TRY(cudaMemsetAsync(base, 0, 4096, st));
+  Q2_CUDA_TRY(cudaMemsetAsync(base + p.nan, 0, (size_t)a.nkv * 128 * sizeof(int), st));
+  Kv8Read r = {};
+  r.k = base + p.k;
+  r.v = base + p.v;
+  r.kc = static_cast<const uint8_t*>(kc);
+  r.vc = static_cast<const uint8_t*>(vc);
+  r.ks = a.ks;
+  r.vs = a.vs;
+  r.tok_stride = 128;
+  r.head_stride = (long long)a.fixed_len * 128;
+  r.batch = 1;
+  r.ntok = a.fixed_len;
+  r.nkv = a.nkv;
+  r.hd = 128;
+  r.max_seq = a.max_seq;
+  r.vnan = reinterpret_cast<int*>(base + p.nan);
+  Q2_TRY(launch_kv8_read(r, Q2_BF16, a.err, st));
+  AttnRows t = {};
+  t.q = a.q;
+  t.q_row_stride = t.out_row_stride = (long long)a.nh * 128;
+  t.k = r.k;
+  t.v = r.v;
+  t.kv_tok_stride = 128;
+  t.kv_head_stride = r.head_stride;
+  t.out = a.out;
+  t.rows = a.ntok;
+  t.nh = a.nh;
+  t.nkv = a.nkv;
+  t.hd = 128;
+  t.base = a.fixed_len - a.ntok + 1;
+  t.row_step = 1;
+  t.scale = a.scale;
+  return launch_attn_tc(t, ws, a.err, st, r.vnan);
+}
+
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
                cudaStream_t st) {
   const SplitPlan p = split_plan(a.ntok, a.nh, a.nkv, hd);
-  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255) || ws_bytes < p.bytes) {
-    set_error("kv8 attention: the workspace is NULL, not 256-byte aligned or smaller than "
-              "q2_kv8_attention_workspace says");
-    return Q2_ERR_INVALID_ARG;
-  }
+  Q2_TRY(check_workspace(ws, ws_bytes, p.bytes));
   if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 29)) {
     set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^29");
     return Q2_ERR_SHAPE;
@@ -962,6 +1042,10 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
   a.scale = scale;
   a.out = out;
   a.err = flag;
+  // (the tcgen05 attention reads q and writes out in 16-byte pieces)
+  if (use_tc(seqlen, nh / nkv, hd, dtype) &&
+      ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0)
+    return attn_tc(a, kc, vc, workspace, workspace_bytes, as_stream(stream));
   return attn(a, (int)hd, dtype, kc, vc, workspace, workspace_bytes, as_stream(stream));
 }
 
@@ -972,9 +1056,15 @@ q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len
   Q2_KV8_ATTN_CHECK("kv8_attention_workspace");
   Q2_CHECK_ARG(bytes, Q2_ERR_INVALID_ARG, "kv8_attention_workspace: NULL bytes");
   Q2_CHECK_ARG(ntok < 65536, Q2_ERR_SHAPE, "kv8_attention_workspace: need ntok < 65536");
-  (void)batch;
-  (void)total_len;
-  *bytes = ntok ? split_plan(ntok, nh, nkv, hd).bytes : 0;
+  Q2_CHECK_ARG(total_len == 0 || (batch == 1 && ntok <= total_len && total_len < (1u << 30)), Q2_ERR_SHAPE,
+               "kv8_attention_workspace: with a total_len, batch must be 1 and ntok at most total_len");
+  *bytes = 0;
+  if (batch == 0 || ntok == 0) return Q2_OK;
+  *bytes = split_plan(ntok, nh, nkv, hd).bytes;
+  if (total_len && use_tc(ntok, nh / nkv, hd, dtype)) {
+    const size_t tc = tc_plan(ntok, total_len, nh, nkv).bytes;
+    if (tc > *bytes) *bytes = tc;  // (either path, as the alignment of q and out has it)
+  }
   return Q2_OK;
 }
 
