@@ -301,33 +301,45 @@ Q8_GROUP = 128   # elements per scale along a linear's reduction
 _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 
-def _here(*ts):
-    """Every tensor on the current CUDA device (the stream of the call is its current stream)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else 0
+_BF16_OR_F32 = (torch.float32, torch.bfloat16)
+
+
+def _here(*ts) -> int:
+    """The stream of a call on these tensors: the current one of the current CUDA device, where
+    every one of them has to lie."""
+    dev = torch._C._cuda_getDevice() if ts[0].is_cuda else -2
     for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"expected tensors on the current CUDA device {dev}, got {t.device}")
+        if t.get_device() != dev:
+            raise ValueError("expected tensors on the current CUDA device, got "
+                             + ", ".join(str(t.device) for t in ts))
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _same_shape(what, *pairs):
-    for t, shape in pairs:
-        if t is not None and tuple(t.shape) != shape:
-            raise ValueError(f"{what}: expected a tensor of shape {shape}, got {tuple(t.shape)}")
-
-
-def _types(what, *pairs):
-    for t, dts in pairs:
-        if t is not None and t.dtype not in dts:
+def _refuse(what, *specs):
+    """The first of (tensor, shape, dtypes) that is not a contiguous tensor of them, as an error."""
+    for t, shape, dts in specs:
+        if t.shape != shape:
+            raise ValueError(f"{what}: expected a tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.dtype not in dts:
             raise TypeError(f"{what}: expected {' or '.join(str(d) for d in dts)}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: expected contiguous tensors")
+    raise ValueError(f"{what}: arguments do not fit together")
+
+
+_F32_ONLY, _I32_ONLY, _U8_ONLY = (torch.float32,), (torch.int32,), (torch.uint8,)
 
 
 def _cache8(what, kc, vc, ks, vs):
-    """The checks of a cache's four tensors; (batch, nkv, max_seq, hd)."""
-    _dense(kc, vc, ks, vs)
-    B, nkv, S, hd = kc.shape
-    _same_shape(what, (vc, (B, nkv, S, hd)), (ks, (B, nkv, -(-S // KV8_BLOCK))), (vs, (B, nkv, -(-S // KV8_BLOCK))))
-    _types(what, (kc, _E4M3), (vc, _E4M3), (ks, (torch.float32,)), (vs, (torch.float32,)))
-    return B, nkv, S, hd
+    """The checks of a cache's four tensors.  (One expression while all is well: a call's checks
+    would otherwise take longer than its launch.)"""
+    shape = kc.shape
+    blocks = (*shape[:-2], -(-shape[-2] // KV8_BLOCK))
+    if not (vc.shape == shape and ks.shape == blocks and vs.shape == blocks
+            and kc.dtype in _E4M3 and vc.dtype in _E4M3
+            and ks.dtype is torch.float32 and vs.dtype is torch.float32
+            and kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        _refuse(what, (kc, shape, _E4M3), (vc, shape, _E4M3), (ks, blocks, _F32_ONLY), (vs, blocks, _F32_ONLY))
 
 
 def _tok_strides(t):
@@ -336,9 +348,10 @@ def _tok_strides(t):
     if t.is_contiguous():
         return None
     _, _, h, d = t.shape
-    if (d > 1 and t.stride(3) != 1) or (h > 1 and t.stride(2) != d):
+    s = t.stride()
+    if (d > 1 and s[3] != 1) or (h > 1 and s[2] != d):
         raise ValueError("the heads of a token must be contiguous")
-    return (ctypes.c_int64 * 2)(t.stride(0), t.stride(1))
+    return (ctypes.c_int64 * 2)(s[0], s[1])
 
 
 def q2_kv8_append(kc, vc, ks, vs, k, v, start):
@@ -346,27 +359,31 @@ def q2_kv8_append(kc, vc, ks, vs, k, v, start):
     positions start[b].. of the 8-bit cache: codes kc, vc [batch, nkv, max_seq, hd] (float8_e4m3fn
     or uint8), scales ks, vs [batch, nkv, ceil(max_seq / 64)] fp32; start int32 [batch], negative =
     inactive.  See q2.h."""
-    B, nkv, S, hd = _cache8("kv8_append", kc, vc, ks, vs)
+    _cache8("kv8_append", kc, vc, ks, vs)
+    B, nkv, S, hd = kc.shape
     T = k.shape[1]
-    _same_shape("kv8_append", (k, (B, T, nkv, hd)), (v, (B, T, nkv, hd)), (start, (B,)))
-    _types("kv8_append", (v, (k.dtype,)), (start, (torch.int32,)))
-    _dense(start)
-    _here(kc, vc, ks, vs, k, v, start)
+    if not (k.shape == (B, T, nkv, hd) and v.shape == k.shape and v.dtype is k.dtype):
+        if v.dtype is not k.dtype:
+            raise TypeError(f"kv8_append: k is {k.dtype}, v {v.dtype}")
+        raise ValueError(f"kv8_append: expected k and v of shape {(B, T, nkv, hd)}, got {tuple(k.shape)}, {tuple(v.shape)}")
+    if not (start.shape == (B,) and start.dtype is torch.int32 and start.is_contiguous()):
+        _refuse("kv8_append", (start, (B,), _I32_ONLY))
     _call("q2_kv8_append", kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), k.data_ptr(), v.data_ptr(),
-          _tok_strides(k), _tok_strides(v), start.data_ptr(), B, T, nkv, hd, S, _dtype(k), _stream())
+          _tok_strides(k), _tok_strides(v), start.data_ptr(), B, T, nkv, hd, S, _dtype(k),
+          _here(kc, vc, ks, vs, k, v, start))
     return kc, vc, ks, vs
 
 
 def q2_kv8_read(k, v, kc, vc, ks, vs, start):
     """k, v [batch, ntok, nkv, hd] = the cache's values at positions start[b].. (see q2.h)."""
-    B, nkv, S, hd = _cache8("kv8_read", kc, vc, ks, vs)
+    _cache8("kv8_read", kc, vc, ks, vs)
+    B, nkv, S, hd = kc.shape
     T = k.shape[1]
-    _same_shape("kv8_read", (k, (B, T, nkv, hd)), (v, (B, T, nkv, hd)), (start, (B,)))
-    _types("kv8_read", (v, (k.dtype,)), (start, (torch.int32,)))
-    _dense(k, v, start)
-    _here(kc, vc, ks, vs, k, v, start)
+    if not (k.shape == (B, T, nkv, hd) and v.shape == k.shape and v.dtype is k.dtype and k.is_contiguous()
+            and v.is_contiguous() and start.shape == (B,) and start.dtype is torch.int32 and start.is_contiguous()):
+        _refuse("kv8_read", (k, (B, T, nkv, hd), _BF16_OR_F32), (v, (B, T, nkv, hd), (k.dtype,)), (start, (B,), _I32_ONLY))
     _call("q2_kv8_read", k.data_ptr(), v.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-          start.data_ptr(), B, T, nkv, hd, S, _dtype(k), _stream())
+          start.data_ptr(), B, T, nkv, hd, S, _dtype(k), _here(kc, vc, ks, vs, k, v, start))
     return k, v
 
 
@@ -376,7 +393,7 @@ _ws_bytes: Dict[Tuple, int] = {}
 def q2_kv8_attention_workspace(batch, ntok, nh, nkv, hd, dtype=torch.bfloat16, total_len=0) -> int:
     """Bytes of workspace that q2_kv8_attention (total_len = 0) or q2_kv8_self_attention
     (batch = 1, ntok = its rows) needs on the current device."""
-    key = (torch.cuda.current_device(), batch, ntok, nh, nkv, hd, dtype, total_len)
+    key = (torch._C._cuda_getDevice(), batch, ntok, nh, nkv, hd, dtype, total_len)
     n = _ws_bytes.get(key)
     if n is None:
         c = _SZ(0)
@@ -387,13 +404,13 @@ def q2_kv8_attention_workspace(batch, ntok, nh, nkv, hd, dtype=torch.bfloat16, t
     return n
 
 
-def _workspace(ws, dev, *args):
+def _workspace(ws, like, *args):
     """The caller's workspace, or one from torch's allocator (stream-ordered, a graph's own)."""
     if ws is None:
-        return torch.empty(q2_kv8_attention_workspace(*args), dtype=torch.uint8, device=dev)
-    _types("workspace", (ws, (torch.uint8,)))
-    _dense(ws)
-    _here(ws)
+        return torch.empty(q2_kv8_attention_workspace(*args), dtype=torch.uint8, device=like.device)
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        _refuse("workspace", (ws, ws.shape, _U8_ONLY))
+    _here(like, ws)
     return ws
 
 
@@ -401,34 +418,35 @@ def q2_kv8_attention(out, q, kc, vc, ks, vs, lens, scale, workspace=None):
     """Causal attention of the last ntok positions of each sequence over its 8-bit cache: q, out
     [batch, ntok, nh, hd] (q's tokens contiguous, any token and sequence stride), lens int32
     [batch] (the new positions included).  See q2.h."""
-    B, nkv, S, hd = _cache8("kv8_attention", kc, vc, ks, vs)
+    _cache8("kv8_attention", kc, vc, ks, vs)
+    B, nkv, S, hd = kc.shape
     _, T, nh, _ = q.shape
-    _same_shape("kv8_attention", (q, (B, T, nh, hd)), (out, (B, T, nh, hd)), (lens, (B,)))
-    _types("kv8_attention", (out, (q.dtype,)), (lens, (torch.int32,)))
-    _dense(out, lens)
-    _here(out, q, kc, vc, ks, vs, lens)
-    ws = _workspace(workspace, q.device, B, T, nh, nkv, hd, q.dtype)
+    if q.shape != (B, T, nh, hd):
+        raise ValueError(f"kv8_attention: expected q of shape {(B, T, nh, hd)}, got {tuple(q.shape)}")
+    if not (out.shape == q.shape and out.dtype is q.dtype and out.is_contiguous() and lens.shape == (B,)
+            and lens.dtype is torch.int32 and lens.is_contiguous()):
+        _refuse("kv8_attention", (out, q.shape, (q.dtype,)), (lens, (B,), _I32_ONLY))
+    stream = _here(out, q, kc, vc, ks, vs, lens)
+    ws = _workspace(workspace, q, B, T, nh, nkv, hd, q.dtype)
     _call("q2_kv8_attention", out.data_ptr(), q.data_ptr(), _tok_strides(q), kc.data_ptr(), vc.data_ptr(),
           ks.data_ptr(), vs.data_ptr(), lens.data_ptr(), B, T, nh, nkv, hd, S, scale, _dtype(q), ws.data_ptr(),
-          ws.numel(), _stream())
+          ws.numel(), stream)
     return out
 
 
 def q2_kv8_self_attention(out, q, kc, vc, ks, vs, total_len, scale, workspace=None):
     """The same for a block of prompt rows of one sequence: q, out [seqlen, nh, hd], kc, vc [nkv,
     max_seq, hd], ks, vs [nkv, blocks]; row i sees keys j <= total_len - seqlen + i.  See q2.h."""
+    _cache8("kv8_self_attention", kc, vc, ks, vs)
     nkv, S, hd = kc.shape
     T, nh, _ = q.shape
-    nb = -(-S // KV8_BLOCK)
-    _dense(out, q, kc, vc, ks, vs)
-    _same_shape("kv8_self_attention", (q, (T, nh, hd)), (out, (T, nh, hd)), (vc, (nkv, S, hd)), (ks, (nkv, nb)),
-                (vs, (nkv, nb)))
-    _types("kv8_self_attention", (out, (q.dtype,)), (kc, _E4M3), (vc, _E4M3), (ks, (torch.float32,)),
-           (vs, (torch.float32,)))
-    _here(out, q, kc, vc, ks, vs)
-    ws = _workspace(workspace, q.device, 1, T, nh, nkv, hd, q.dtype, total_len)
+    if not (q.shape == (T, nh, hd) and out.shape == q.shape and out.dtype is q.dtype and q.is_contiguous()
+            and out.is_contiguous()):
+        _refuse("kv8_self_attention", (q, (T, nh, hd), _BF16_OR_F32), (out, (T, nh, hd), (q.dtype,)))
+    stream = _here(out, q, kc, vc, ks, vs)
+    ws = _workspace(workspace, q, 1, T, nh, nkv, hd, q.dtype, total_len)
     _call("q2_kv8_self_attention", out.data_ptr(), q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
-          vs.data_ptr(), T, total_len, nh, nkv, hd, S, scale, _dtype(q), ws.data_ptr(), ws.numel(), _stream())
+          vs.data_ptr(), T, total_len, nh, nkv, hd, S, scale, _dtype(q), ws.data_ptr(), ws.numel(), stream)
     return out
 
 
@@ -438,15 +456,15 @@ def q2_quantize_q8(codes, scales, x, block_rows=1):
     (weights).  See q2.h."""
     rows, cols = x.shape
     groups = -(-cols // Q8_GROUP)
-    _same_shape("quantize_q8", (codes, (rows, cols)),
-                (scales, (groups, rows) if block_rows == 1 else (-(-rows // 128), groups)))
-    _types("quantize_q8", (codes, _E4M3), (scales, (torch.float32,)))
-    _dense(codes, scales)
-    if cols > 1 and x.stride(1) != 1:
+    shape = (groups, rows) if block_rows == 1 else (-(-rows // 128), groups)
+    if not (codes.shape == x.shape and codes.dtype in _E4M3 and codes.is_contiguous() and scales.shape == shape
+            and scales.dtype is torch.float32 and scales.is_contiguous()):
+        _refuse("quantize_q8", (codes, x.shape, _E4M3), (scales, shape, _F32_ONLY))
+    s = x.stride()
+    if cols > 1 and s[1] != 1:
         raise ValueError("the elements of a row must be contiguous")
-    _here(codes, scales, x)
-    _call("q2_quantize_q8", codes.data_ptr(), scales.data_ptr(), x.data_ptr(), rows, cols, x.stride(0), block_rows,
-          _dtype(x), _stream())
+    _call("q2_quantize_q8", codes.data_ptr(), scales.data_ptr(), x.data_ptr(), rows, cols, s[0], block_rows,
+          _dtype(x), _here(codes, scales, x))
     return codes, scales
 
 
@@ -456,14 +474,18 @@ def q2_linear_q8(out, xq, xs, wq, ws, bias=None):
     M, K = xq.shape
     N = wq.shape[0]
     groups = -(-K // Q8_GROUP)
-    _same_shape("linear_q8", (out, (M, N)), (xs, (groups, M)), (wq, (N, K)), (ws, (-(-N // 128), groups)),
-                (bias, (N,)))
-    _types("linear_q8", (xq, _E4M3), (wq, _E4M3), (xs, (torch.float32,)), (ws, (torch.float32,)),
-           (bias, (out.dtype,)))
-    _dense(out, xq, xs, wq, ws, bias)
-    _here(out, xq, xs, wq, ws, bias)
+    wshape = (-(-N // 128), groups)
+    if not (out.shape == (M, N) and xs.shape == (groups, M) and wq.shape == (N, K) and ws.shape == wshape
+            and xq.dtype in _E4M3 and wq.dtype in _E4M3 and xs.dtype is torch.float32 and ws.dtype is torch.float32
+            and out.is_contiguous() and xq.is_contiguous() and xs.is_contiguous() and wq.is_contiguous()
+            and ws.is_contiguous()):
+        _refuse("linear_q8", (out, (M, N), _BF16_OR_F32), (xq, (M, K), _E4M3), (xs, (groups, M), _F32_ONLY),
+                (wq, (N, K), _E4M3), (ws, wshape, _F32_ONLY))
+    if bias is not None and not (bias.shape == (N,) and bias.dtype is out.dtype and bias.is_contiguous()):
+        _refuse("linear_q8", (bias, (N,), (out.dtype,)))
+    stream = _here(out, xq, xs, wq, ws) if bias is None else _here(out, xq, xs, wq, ws, bias)
     _call("q2_linear_q8", out.data_ptr(), xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-          None if bias is None else bias.data_ptr(), M, N, K, _dtype(out), _stream())
+          None if bias is None else bias.data_ptr(), M, N, K, _dtype(out), stream)
     return out
 
 

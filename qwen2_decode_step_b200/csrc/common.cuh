@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <string>
 #include <utility>
 
@@ -273,6 +274,21 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+}  // namespace q2
+
+namespace q2 {
+// Whether this is the first call on the current device for `done` (one bit per
+// device; a kernel's attributes are set once).  Devices past 63 always set them.
+inline bool first_on_device(std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return true;
+  return (done.load(std::memory_order_acquire) >> dev & 1) == 0;
+}
+inline void done_on_device(std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev <= 63)
+    done.fetch_or(1ull << dev, std::memory_order_release);
 }
 }  // namespace q2
 

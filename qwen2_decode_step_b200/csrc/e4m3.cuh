@@ -47,33 +47,4 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < INFINITY ? a : 0.f;
 }
 
-// Sixteen consecutive elements of storage type T as fp32, of which the first n
-// (<= 16) exist; the others read as 0.  VEC: 16-byte aligned and n == 16.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load16(const T* p, int n, float* f) {
-  if constexpr (VEC) {
-    constexpr int kV = Storage<T>::kVec;
-#pragma unroll
-    for (int i = 0; i < 16 / kV; ++i) unpack16<T>(reinterpret_cast<const uint4*>(p)[i], f + i * kV);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = i < n ? to_f(p[i]) : 0.f;
-  }
-}
-
-// Sixteen values to codes at p, of which the first n exist.
-template <bool VEC>
-__device__ __forceinline__ void store16_e4m3(uint8_t* p, int n, const float* f) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = e4m3x4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-  if constexpr (VEC) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
-  }
-}
-
 }  // namespace q2

@@ -32,10 +32,13 @@ __device__ __forceinline__ float block_scale(float amax) {
 }
 
 struct Kv8Append {
-  uint8_t* c[2];      // codes of K, of V
-  float* s[2];        // scales
-  const void* x[2];   // new rows
-  long long seq_stride[2], tok_stride[2];  // of x, in elements
+  uint8_t* kc;
+  uint8_t* vc;
+  float* ks;
+  float* vs;
+  const void* k;
+  const void* v;
+  long long k_seq_stride, k_tok_stride, v_seq_stride, v_tok_stride;  // of k and v, in elements
   const int32_t* start;
   int batch, ntok, nkv, max_seq, nblk;
   int* err;
@@ -44,18 +47,19 @@ struct Kv8Append {
 // One CTA writes one block of 64 positions (those of its rows that are new) of
 // one kv head of K or of V: it owns the block's codes and scale, so nothing
 // races.  Bound by HBM for long prompts (bf16 in, a byte out) and by launch
-// latency for one token.  An item is 16 elements of a row: one 16-byte store
-// of codes; a thread keeps its (at most two, for hd 128) items in registers
-// between the maximum and the conversion, so the new rows are read once.
+// latency for one token.  An item is 16 bytes of a new row, so a warp's loads
+// are whole lines; a thread keeps its items (at most eight, fp32 and hd 128) in
+// registers between the maximum and the conversion: the rows are read once.
 template <typename T, int HD, bool VEC>
 __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8Append a) {
-  constexpr int kItemsRow = HD / 16;
-  constexpr int kItems = kBlk * kItemsRow;
-  constexpr int kPer = (kItems + kThreads - 1) / kThreads;
+  constexpr int kV = Storage<T>::kVec;
+  constexpr int kItemsRow = HD / kV;
+  constexpr int kPer = (kBlk * kItemsRow + kThreads - 1) / kThreads;
   __shared__ float wmax[kThreads / 32];
   pdl_launch_dependents();
   pdl_wait();
-  const int kv = blockIdx.y & 1, g = blockIdx.y >> 1, b = blockIdx.z, tid = threadIdx.x;
+  const bool isv = blockIdx.y & 1;
+  const int g = blockIdx.y >> 1, b = blockIdx.z, tid = threadIdx.x;
   const int start = a.start[b];
   if (start < 0) return;  // an inactive sequence
   if (a.ntok > a.max_seq - start) {
@@ -67,24 +71,36 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8Append a)
   const int lo = max(start, p0), hi = min(start + a.ntok, p0 + kBlk);  // the new ones
   if (lo >= hi) return;
   const size_t head = (size_t)b * a.nkv + g;
-  uint8_t* codes = a.c[kv] + (head * a.max_seq + p0) * HD;
-  float* scale = a.s[kv] + head * a.nblk + blk;
-  const T* x = reinterpret_cast<const T*>(a.x[kv]) + (long long)b * a.seq_stride[kv] + (long long)g * HD;
+  uint8_t* codes = (isv ? a.vc : a.kc) + (head * a.max_seq + p0) * HD;
+  float* scale = (isv ? a.vs : a.ks) + head * a.nblk + blk;
+  const long long tok_stride = isv ? a.v_tok_stride : a.k_tok_stride;
+  const T* x = reinterpret_cast<const T*>(isv ? a.v : a.k) + (long long)b * (isv ? a.v_seq_stride : a.k_seq_stride) +
+               (long long)(lo - start) * tok_stride + (long long)g * HD;
 
-  float f[kPer][16];
-  float m = 0.f;
+  float f[kPer][kV];
   const int n = (hi - lo) * kItemsRow;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int it = tid + i * kThreads;
+    const T* p = x + (long long)(it / kItemsRow) * tok_stride + (it % kItemsRow) * kV;
     if (it < n) {
-      load16<T, VEC>(x + (long long)(lo - start + it / kItemsRow) * a.tok_stride[kv] + (it % kItemsRow) * 16, 16,
-                     f[i]);
+      if constexpr (VEC) {
+        unpack16<T>(*reinterpret_cast<const uint4*>(p), f[i]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) m = fmaxf(m, finite_abs(f[i][j]));
+        for (int j = 0; j < kV; ++j) f[i][j] = to_f(p[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) f[i][j] = 0.f;
     }
   }
   const float before = lo > p0 ? *scale : 0.f;
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+#pragma unroll
+    for (int j = 0; j < kV; ++j) m = fmaxf(m, finite_abs(f[i][j]));
   m = warp_max(m);
   if ((tid & 31) == 0) wmax[tid >> 5] = m;
   __syncthreads();
@@ -95,35 +111,40 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8Append a)
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int it = tid + i * kThreads;
-    if (it < n) {
+    if (it >= n) break;
+    uint32_t w[kV / 4];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) f[i][j] *= inv;
-      store16_e4m3<true>(codes + (size_t)(lo - p0) * HD + (size_t)it * 16, 16, f[i]);
-    }
+    for (int j = 0; j < kV / 4; ++j)
+      w[j] = e4m3x4(f[i][4 * j] * inv, f[i][4 * j + 1] * inv, f[i][4 * j + 2] * inv, f[i][4 * j + 3] * inv);
+    uint8_t* o = codes + (size_t)(lo - p0) * HD + (size_t)it * kV;
+    if constexpr (kV == 8)
+      *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(o) = w[0];
   }
   if (lo > p0 && s != before) {  // the earlier codes of the block move to the new scale
     const float ratio = before * inv;
-    for (int it = tid; it < (lo - p0) * kItemsRow; it += kThreads) {
-      uint4* p = reinterpret_cast<uint4*>(codes) + it;
-      const uint4 v = *p;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float o[16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) e4m3x4_to_f(w[j], o + 4 * j);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] *= ratio;
-      store16_e4m3<true>(reinterpret_cast<uint8_t*>(p), 16, o);
+    for (int it = tid; it < (lo - p0) * (HD / 4); it += kThreads) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(codes) + it;
+      float o[4];
+      e4m3x4_to_f(*p, o);
+      *p = e4m3x4(o[0] * ratio, o[1] * ratio, o[2] * ratio, o[3] * ratio);
     }
   }
   if (tid == 0) *scale = s;  // every thread has read it: the barrier above
 }
 
 // One CTA reads 64 consecutive positions of one sequence (all kv heads) of K
-// or of V.  Bound by HBM: a byte in, two or four out per element.
+// or of V.  Bound by HBM: a byte in, two or four out per element.  A thread's
+// item is 16 bytes of output, so a warp's stores are whole lines (with 16 codes
+// an item they were 64 bytes apart: 22 us instead of READ_US for 32768 positions
+// of two heads to fp32); its loads are issued before the first store.
 template <typename T, int HD, bool VEC>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8Read a, int nblk, int* err) {
-  constexpr int kItemsRow = HD / 16;
+  constexpr int kV = Storage<T>::kVec;   // 4 or 8 elements
+  constexpr int kItemsRow = HD / kV;
   constexpr int kItems = kBlk * kItemsRow;
+  constexpr int kPer = (kItems + kThreads - 1) / kThreads;
   pdl_launch_dependents();
   pdl_wait();
   const bool isv = blockIdx.y & 1;
@@ -139,20 +160,32 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8Read a, int
     const uint8_t* codes = (isv ? a.vc : a.kc) + (head * a.max_seq + start + t0) * HD;
     const float* scale = (isv ? a.vs : a.ks) + head * nblk;
     T* out = reinterpret_cast<T*>(isv ? a.v : a.k) + (long long)b * a.seq_stride + (long long)g * a.head_stride;
+    uint2 w[kPer];
+    float s[kPer];
 #pragma unroll
-    for (int i = 0; i < (kItems + kThreads - 1) / kThreads; ++i) {
+    for (int i = 0; i < kPer; ++i) {
+      const int it = threadIdx.x + i * kThreads;
+      w[i] = make_uint2(0u, 0u);
+      s[i] = 0.f;
+      if (it < n) {
+        if constexpr (kV == 8)
+          w[i] = __ldg(reinterpret_cast<const uint2*>(codes) + it);
+        else
+          w[i].x = __ldg(reinterpret_cast<const uint32_t*>(codes) + it);
+        s[i] = __ldg(scale + (start + t0 + it / kItemsRow) / kBlk);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
       const int it = threadIdx.x + i * kThreads;
       if (it >= n) break;
-      const int t = t0 + it / kItemsRow, d = (it % kItemsRow) * 16;
-      const uint4 v = reinterpret_cast<const uint4*>(codes)[it];
-      const float s = scale[(start + t) / kBlk];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float f[16];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) e4m3x4_to_f(w[j], f + 4 * j);
+      const int t = t0 + it / kItemsRow, d = (it % kItemsRow) * kV;
+      float f[kV];
+      e4m3x4_to_f(w[i].x, f);
+      if constexpr (kV == 8) e4m3x4_to_f(w[i].y, f + 4);
       if (isv && a.vnan) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
+        for (int j = 0; j < kV; ++j)
           if (isnan(f[j])) {
             f[j] = 0.f;
             atomicMax(a.vnan + g * HD + d + j, INT32_MAX - (start + t));
@@ -160,14 +193,12 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8Read a, int
       }
       T* o = out + (long long)t * a.tok_stride + d;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] *= s;
+      for (int j = 0; j < kV; ++j) f[j] *= s[i];
       if constexpr (VEC) {
-        constexpr int kV = Storage<T>::kVec;
-#pragma unroll
-        for (int j = 0; j < 16 / kV; ++j) reinterpret_cast<uint4*>(o)[j] = pack16<T>(f + j * kV);
+        *reinterpret_cast<uint4*>(o) = pack16<T>(f);
       } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = from_f<T>(f[j]);
+        for (int j = 0; j < kV; ++j) o[j] = from_f<T>(f[j]);
       }
     }
   }
@@ -233,19 +264,17 @@ q2_status q2_kv8_append(void* kc, void* vc, float* ks, float* vs, const void* k,
   Q2_KV8_CHECK("kv8_append");
   int* flag = op_error_flag();
   Q2_CHECK_ARG(flag, Q2_ERR_CUDA, "cannot resolve the device error flag");
-  const long long dense[2] = {(long long)(ntok * nkv * hd), (long long)(nkv * hd)};
   Kv8Append a;
-  a.c[0] = static_cast<uint8_t*>(kc);
-  a.c[1] = static_cast<uint8_t*>(vc);
-  a.s[0] = ks;
-  a.s[1] = vs;
-  a.x[0] = k;
-  a.x[1] = v;
-  for (int i = 0; i < 2; ++i) {
-    const int64_t* s = i ? v_strides : k_strides;
-    a.seq_stride[i] = s ? s[0] : dense[0];
-    a.tok_stride[i] = s ? s[1] : dense[1];
-  }
+  a.kc = static_cast<uint8_t*>(kc);
+  a.vc = static_cast<uint8_t*>(vc);
+  a.ks = ks;
+  a.vs = vs;
+  a.k = k;
+  a.v = v;
+  a.k_seq_stride = k_strides ? k_strides[0] : (long long)(ntok * nkv * hd);
+  a.k_tok_stride = k_strides ? k_strides[1] : (long long)(nkv * hd);
+  a.v_seq_stride = v_strides ? v_strides[0] : (long long)(ntok * nkv * hd);
+  a.v_tok_stride = v_strides ? v_strides[1] : (long long)(nkv * hd);
   a.start = start;
   a.batch = (int)batch;
   a.ntok = (int)ntok;
@@ -254,8 +283,8 @@ q2_status q2_kv8_append(void* kc, void* vc, float* ks, float* vs, const void* k,
   a.nblk = (int)((max_seq + kBlk - 1) / kBlk);
   a.err = flag;
   const size_t es = dtype == Q2_BF16 ? 2 : 4;
-  const bool vec = rows_aligned(k, a.seq_stride[0], a.tok_stride[0], es) &&
-                   rows_aligned(v, a.seq_stride[1], a.tok_stride[1], es);
+  const bool vec = rows_aligned(k, a.k_seq_stride, a.k_tok_stride, es) &&
+                   rows_aligned(v, a.v_seq_stride, a.v_tok_stride, es);
   const bool bf = dtype == Q2_BF16;
   cudaStream_t st = as_stream(stream);
   switch (hd) {

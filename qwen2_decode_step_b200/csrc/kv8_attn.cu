@@ -817,7 +817,11 @@ template <typename T, int HD, int NT>
 q2_status split_t(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaStream_t st) {
   using SM = SplitSmem<HD, NT>;
   auto* kernel = kv8_split_kernel<T, HD, NT>;
-  Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
+  static std::atomic<uint64_t> done{0};
+  if (first_on_device(done)) {
+    Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
+    done_on_device(done);
+  }
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)a.batch * a.nkv * a.max_seq;
   Q2_TRY(make_tmap_2d_u8(&km, kc, rows, HD, HD, kKeys, HD, HD));

@@ -142,8 +142,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 template <typename T>
-__device__ __forceinline__ void store_out(const Q8Lin& a, int m, int n, float y) {
-  if (a.bias) y += to_f(reinterpret_cast<const T*>(a.bias)[n]);
+__device__ __forceinline__ void store_out(const Q8Lin& a, int m, int n, float y, bool bias) {
+  if (bias && a.bias) y += to_f(reinterpret_cast<const T*>(a.bias)[n]);
   reinterpret_cast<T*>(a.out)[(size_t)m * a.N + n] = from_f<T>(y);
 }
 
@@ -282,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kNCh = kHalf / kCh;
     constexpr int kTwo = kNCh > 1 ? 2 : 1;             // TMEM loads in flight
     constexpr int kWs = WIDE && BN == 192 ? 3 : 1;     // weight scales of the warp's columns: 96 may straddle a block
+    constexpr int kV = Storage<T>::kVec;
     constexpr int kAhead = 2;                          // groups whose scales are read at a time
     const int q = warp & 3, half = (warp - kEpiWarp0) / 4;
     const int l = 32 * q + lane;                       // this thread's TMEM lane
@@ -322,8 +323,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (w.t < a.tiles) {
       const int r0 = w.lt * kLanes, c0 = w.ct * BN + half * kHalf;
       float2 sum[kHalf / 2];
+      // wide, 16-byte output rows: the sums begin at the bias (added at the end,
+      // its loads lay bare in the store: 20 of 151 us)
+      const bool bias_in = WIDE && a.tma_out && a.bias;
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) sum[i] = make_float2(0.f, 0.f);
+      for (int i = 0; i < kHalf / kV; ++i) {
+        float y[kV];
+        if (bias_in && c0 + i * kV < a.N) {
+          unpack16<T>(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.bias) + c0) + i), y);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kV; ++j) y[j] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kV / 2; ++j) sum[i * kV / 2 + j] = make_float2(y[2 * j], y[2 * j + 1]);
+      }
       for (int gg = g0; gg < g1; gg += kAhead) {
         float xn[kAhead], wn[kAhead][kWs];
         load_scales(xn, wn, gg + kAhead);
@@ -398,7 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (Stored by the threads, a row per lane, a tile's 64 KB took 13000
           // cycles against its 12 groups' 6100.)
           constexpr int kPer = 128 / (int)sizeof(T);     // columns of a part
-          constexpr int kV = Storage<T>::kVec;
           uint8_t* turn = smem + SM::kTurn + (size_t)(warp - kEpiWarp0) * 4096;
 #pragma unroll
           for (int p = 0; p < (kHalf + kPer - 1) / kPer; ++p) {
@@ -412,15 +425,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < kV / 2; ++e) {
                 y[2 * e] = sum[(p * kPer + j * kV) / 2 + e].x;
                 y[2 * e + 1] = sum[(p * kPer + j * kV) / 2 + e].y;
-              }
-              if (a.bias) {
-                const int n = c0 + p * kPer + j * kV;
-                float b[kV];
-                unpack16<T>(n < a.N ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.bias) + n))
-                                    : make_uint4(0u, 0u, 0u, 0u),
-                            b);
-#pragma unroll
-                for (int e = 0; e < kV; ++e) y[e] += b[e];
               }
               *reinterpret_cast<uint4*>(turn + lane * 128 + ((j ^ (lane & 7)) << 4)) = pack16<T>(y);
             }
@@ -449,8 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (const int m = r0 + l; m < a.M) {
 #pragma unroll
           for (int i = 0; i < kHalf / 2; ++i) {
-            if (c0 + 2 * i < a.N) store_out<T>(a, m, c0 + 2 * i, sum[i].x);
-            if (c0 + 2 * i + 1 < a.N) store_out<T>(a, m, c0 + 2 * i + 1, sum[i].y);
+            if (c0 + 2 * i < a.N) store_out<T>(a, m, c0 + 2 * i, sum[i].x, !bias_in);
+            if (c0 + 2 * i + 1 < a.N) store_out<T>(a, m, c0 + 2 * i + 1, sum[i].y, !bias_in);
           }
         }
       } else {
@@ -491,10 +495,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int r = 1; r < kClusterMax; ++r)
           if (r < a.csize) y = make_float4(y.x + v[r].x, y.y + v[r].y, y.z + v[r].z, y.w + v[r].w);
-        store_out<T>(a, m, n, y.x);
-        if (n + 1 < a.N) store_out<T>(a, m, n + 1, y.y);
-        if (n + 2 < a.N) store_out<T>(a, m, n + 2, y.z);
-        if (n + 3 < a.N) store_out<T>(a, m, n + 3, y.w);
+        store_out<T>(a, m, n, y.x, true);
+        if (n + 1 < a.N) store_out<T>(a, m, n + 1, y.y, true);
+        if (n + 2 < a.N) store_out<T>(a, m, n + 2, y.z, true);
+        if (n + 3 < a.N) store_out<T>(a, m, n + 3, y.w, true);
       }
       cluster_sync();  // no CTA leaves while another reads its tile
     }
@@ -512,14 +516,18 @@ template <typename T, bool WIDE, int BN, int STAGES>
 q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t st) {
   using SM = Q8Smem<WIDE, BN, STAGES>;
   auto* kernel = q8_linear_kernel<T, WIDE, BN, STAGES>;
-  Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
-  // the register split draws on what the kernel is launched with: fewer would
-  // leave setmaxnreg.inc waiting
-  cudaFuncAttributes fa;
-  Q2_CUDA_TRY(cudaFuncGetAttributes(&fa, kernel));
-  if (fa.numRegs * kThreads < kRegsLow * kEpiWarp0 * 32 + kRegsHigh * kEpiWarps * 32) {
-    set_error("linear_q8: the kernel was built with too few registers for its split");
-    return Q2_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (first_on_device(done)) {
+    Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
+    // the register split draws on what the kernel is launched with: fewer would
+    // leave setmaxnreg.inc waiting
+    cudaFuncAttributes fa;
+    Q2_CUDA_TRY(cudaFuncGetAttributes(&fa, kernel));
+    if (fa.numRegs * kThreads < kRegsLow * kEpiWarp0 * 32 + kRegsHigh * kEpiWarps * 32) {
+      set_error("linear_q8: the kernel was built with too few registers for its split");
+      return Q2_ERR_CUDA;
+    }
+    done_on_device(done);
   }
   a.lane_tiles = ((WIDE ? a.M : a.N) + kLanes - 1) / kLanes;
   const long long tiles = (long long)a.lane_tiles * (((WIDE ? a.N : a.M) + BN - 1) / BN);

@@ -19,7 +19,6 @@ namespace q2 {
 namespace {
 
 constexpr int kGroup = Q2_Q8_GROUP;
-constexpr int kItemsGroup = kGroup / 16;  // eight lanes hold a row of a group
 
 struct Quant {
   const void* x;
@@ -29,113 +28,156 @@ struct Quant {
   int rows, cols, groups;
 };
 
-// The largest finite magnitude of sixteen elements (fmaxf passes over NaN);
+// A lane's share of a row of a group: vectors of 16 bytes (kV elements, so that
+// a warp's loads and stores are whole lines), or, where rows do not start on 16
+// bytes, elements 32 apart (a warp's loads are neighbours again).
+template <typename T, bool VEC>
+struct Share {
+  static constexpr int kV = VEC ? Storage<T>::kVec : 4;   // elements of a lane
+  static constexpr int kLanes = kGroup / kV;              // lanes of a row: 32, or 16 (bf16 vectors)
+  static constexpr int kRows = 32 / kLanes;               // rows of a warp's step
+  static __device__ __forceinline__ void load(const T* row, int c0, int cols, float* f) {
+    const int l = threadIdx.x % kLanes;
+    if constexpr (VEC) {
+      const int c = c0 + l * kV;
+      if (c < cols) {
+        unpack16<T>(*reinterpret_cast<const uint4*>(row + c), f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) f[j] = 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) f[j] = c0 + l + 32 * j < cols ? to_f(row[c0 + l + 32 * j]) : 0.f;
+    }
+  }
+  static __device__ __forceinline__ void store(uint8_t* row, int c0, int cols, const float* f) {
+    const int l = threadIdx.x % kLanes;
+    if constexpr (VEC) {
+      const int c = c0 + l * kV;
+      if (c < cols) {
+        const uint32_t w = e4m3x4(f[0], f[1], f[2], f[3]);
+        if constexpr (kV == 8)
+          *reinterpret_cast<uint2*>(row + c) = make_uint2(w, e4m3x4(f[4], f[5], f[6], f[7]));
+        else
+          *reinterpret_cast<uint32_t*>(row + c) = w;
+      }
+    } else {
+      const uint32_t w = e4m3x4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+      for (int j = 0; j < kV; ++j)
+        if (c0 + l + 32 * j < cols) row[c0 + l + 32 * j] = (uint8_t)(w >> (8 * j));
+    }
+  }
+};
+
+// The largest finite magnitude of a lane's N elements (fmaxf passes over NaN);
 // `inf` says whether an infinity was among them, which is rare and settled out
 // of the way of the others.
-__device__ __forceinline__ float thread_amax(const float* f, bool* inf) {
+template <int N>
+__device__ __forceinline__ float lane_amax(const float* f, bool* inf) {
   float m = fabsf(f[0]);
 #pragma unroll
-  for (int j = 1; j < 16; ++j) m = fmaxf(m, fabsf(f[j]));
+  for (int j = 1; j < N; ++j) m = fmaxf(m, fabsf(f[j]));
   *inf = m == INFINITY;
   if (*inf) {
     m = 0.f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) m = fmaxf(m, finite_abs(f[j]));
+    for (int j = 0; j < N; ++j) m = fmaxf(m, finite_abs(f[j]));
   }
   return m;
 }
 
-// x * (448 / a) of sixteen elements, in place (infinities go to +-448 here:
-// times lo they would become NaN).
-__device__ __forceinline__ void to_code_range(float* f, float a, bool inf) {
+// x * (448 / a) of N elements, in place (infinities go to +-448 here: times lo
+// they would become NaN).
+template <int N>
+__device__ __forceinline__ void to_code_range(float* f, float a, float hi, float lo, bool inf) {
   if (inf) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < N; ++j)
       if (fabsf(f[j]) == INFINITY) f[j] = copysignf(a, f[j]);
   }
-  const float hi = __fdiv_rn(kE4m3Max, a);
-  const float lo = __fdiv_rn(fmaf(-hi, a, kE4m3Max), a);
 #pragma unroll
-  for (int j = 0; j < 16; ++j) f[j] = fmaf(f[j], hi, f[j] * lo);
+  for (int j = 0; j < N; ++j) f[j] = fmaf(f[j], hi, f[j] * lo);
+}
+__device__ __forceinline__ void quotient(float a, float* hi, float* lo) {
+  *hi = __fdiv_rn(kE4m3Max, a);
+  *lo = __fdiv_rn(fmaf(-*hi, a, kE4m3Max), a);
 }
 
-// Rows: a CTA takes 32 rows x kRowGroups groups.  A warp takes one group of
-// four rows (eight lanes each), so the CTA's scales of a group are 32
-// consecutive floats of the [groups][rows] array and every row segment it
-// reads is 256 bytes of bf16; all of a thread's loads are issued before the
-// first is used.
+// Rows: a CTA takes 16 (fp32 and unaligned rows: 8) rows x kRowGroups groups, a
+// warp two rows (one).  CTAs go along a row first, so that the machine reads
+// whole pages; all of a thread's loads are issued before the first is used.
 constexpr int kRowGroups = 4;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) quant_rows_kernel(const Quant a) {
+  using S = Share<T, VEC>;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.x * 32 + warp * 4 + (lane >> 3);
-  const int g0 = blockIdx.y * kRowGroups;
-  const bool in = row < a.rows;
-  const T* x = reinterpret_cast<const T*>(a.x) + (long long)row * a.stride;
-  float f[kRowGroups][16];
+  const int chunks = (a.groups + kRowGroups - 1) / kRowGroups;
+  const int rc = blockIdx.x / chunks, g0 = (blockIdx.x - rc * chunks) * kRowGroups;
+  const int row = (rc * 8 + warp) * S::kRows + lane / S::kLanes;
+  const int cols = row < a.rows ? a.cols : 0;
+  float f[kRowGroups][S::kV];
 #pragma unroll
-  for (int i = 0; i < kRowGroups; ++i) {
-    const int c = (g0 + i) * kGroup + (lane & 7) * 16;
-    const int n = in ? min(16, a.cols - c) : 0;
-    if (n > 0) {
-      load16<T, VEC>(x + c, n, f[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) f[i][j] = 0.f;
-    }
-  }
+  for (int i = 0; i < kRowGroups; ++i)
+    S::load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, (g0 + i) * kGroup, cols, f[i]);
 #pragma unroll
   for (int i = 0; i < kRowGroups; ++i) {
     bool inf;
-    float m = thread_amax(f[i], &inf);
+    float m = lane_amax<S::kV>(f[i], &inf);
 #pragma unroll
-    for (int o = 1; o < kItemsGroup; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < S::kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = fmaxf(m, 0x1p-100f);
-    const int c = (g0 + i) * kGroup + (lane & 7) * 16;
-    const int n = in ? min(16, a.cols - c) : 0;
-    to_code_range(f[i], m, inf);
-    if (n > 0) store16_e4m3<VEC>(a.codes + (size_t)row * a.cols + c, n, f[i]);
-    if (in && (lane & 7) == 0 && g0 + i < a.groups)
+    float hi, lo;
+    quotient(m, &hi, &lo);
+    to_code_range<S::kV>(f[i], m, hi, lo, inf);
+    S::store(a.codes + (size_t)row * a.cols, (g0 + i) * kGroup, cols, f[i]);
+    if (lane % S::kLanes == 0 && row < a.rows && g0 + i < a.groups)
       a.scales[(size_t)(g0 + i) * a.rows + row] = __fdiv_rn(m, kE4m3Max);
   }
 }
 
-// Blocks: one CTA per 128 x 128 block, held in registers between the maximum
-// and the conversion (32 elements per thread).
+// Blocks: one CTA of 16 warps per 128 x 128 block, held in registers between
+// the maximum and the conversion (32 elements per thread).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(512) quant_blocks_kernel(const Quant a) {
+  using S = Share<T, VEC>;
+  constexpr int kSteps = 128 / (16 * S::kRows);
   __shared__ float wmax[16];
   pdl_launch_dependents();
   pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = blockIdx.x, rb = blockIdx.y;
-  const int c = g * kGroup + (threadIdx.x & 7) * 16, r0 = rb * 128 + (threadIdx.x >> 3);
-  const int n = min(16, a.cols - c);
-  float f[2][16];
-  bool inf[2];
+  const int row0 = rb * 128 + warp * S::kRows + lane / S::kLanes;
+  float f[kSteps][S::kV];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int row = row0 + 16 * S::kRows * i;
+    S::load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, g * kGroup, row < a.rows ? a.cols : 0, f[i]);
+  }
+  bool any_inf = false;
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = r0 + 64 * i;
-    if (row < a.rows && n > 0) {
-      load16<T, VEC>(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride + c, n, f[i]);
-      m = fmaxf(m, thread_amax(f[i], &inf[i]));
-    }
+  for (int i = 0; i < kSteps; ++i) {
+    bool inf;
+    m = fmaxf(m, lane_amax<S::kV>(f[i], &inf));
+    any_inf |= inf;
   }
   m = warp_max(m);
-  if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
+  if (lane == 0) wmax[warp] = m;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < 16; ++w) m = fmaxf(m, wmax[w]);
   m = fmaxf(m, 0x1p-100f);
+  float hi, lo;
+  quotient(m, &hi, &lo);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int row = r0 + 64 * i;
-    if (row < a.rows && n > 0) {
-      to_code_range(f[i], m, inf[i]);
-      store16_e4m3<VEC>(a.codes + (size_t)row * a.cols + c, n, f[i]);
-    }
+  for (int i = 0; i < kSteps; ++i) {
+    const int row = row0 + 16 * S::kRows * i;
+    to_code_range<S::kV>(f[i], m, hi, lo, any_inf);
+    S::store(a.codes + (size_t)row * a.cols, g * kGroup, row < a.rows ? a.cols : 0, f[i]);
   }
   if (threadIdx.x == 0) a.scales[(size_t)rb * a.groups + g] = __fdiv_rn(m, kE4m3Max);
 }
@@ -143,7 +185,13 @@ __global__ void __launch_bounds__(512) quant_blocks_kernel(const Quant a) {
 template <typename T>
 q2_status quant_t(const Quant& a, int block_rows, bool vec, cudaStream_t st) {
   if (block_rows == 1) {
-    const dim3 grid((a.rows + 31) / 32, (a.groups + kRowGroups - 1) / kRowGroups);
+    const int per = 8 * (vec ? Share<T, true>::kRows : Share<T, false>::kRows);
+    const long long ctas = (long long)((a.rows + per - 1) / per) * ((a.groups + kRowGroups - 1) / kRowGroups);
+    if (ctas >= (1ll << 31)) {
+      set_error("quantize_q8: too many rows and columns for one call");
+      return Q2_ERR_SHAPE;
+    }
+    const dim3 grid((unsigned)ctas);
     Q2_LAUNCH(vec ? quant_rows_kernel<T, true> : quant_rows_kernel<T, false>, grid, dim3(256), 0, st, true, a);
   } else {
     const dim3 grid(a.groups, (a.rows + 127) / 128);
