@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------------- MMA
       // The whole warp walks the loop and one elected lane issues, so that the
       // descriptors stay in uniform registers (from one lane's own registers a
-      // group's six instructions took 400 cycles to issue).
+      // group's six instructions took 400 cycles to issue).  It polls: asleep it
+      // woke so late that 61 tokens x 151936 features took 65 us, not 46.
       constexpr uint32_t idesc = idesc_e4m3(BN);
       const uint64_t da0 = sw128_desc(smem), db0 = sw128_desc(smem + SM::kA);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -245,8 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0, aph = 0;
       for (int t = first; t < a.tiles; t += step) {
         for (int g = g0; g < g1; ++g) {
-          if (!tc_wait_asleep(&acc_empty[acc], aph ^ 1u) && lane == 0) atomicOr(a.err, kErrTimeout);
-          if (!tc_wait_asleep(&full[s], ph) && lane == 0) atomicOr(a.err, kErrTimeout);
+          if (!tc_wait_poll(&acc_empty[acc], aph ^ 1u) && lane == 0) atomicOr(a.err, kErrTimeout);
+          if (!tc_wait_poll(&full[s], ph) && lane == 0) atomicOr(a.err, kErrTimeout);
           tc_fence_after();
           if (elect_one()) {
             const uint64_t at = (uint64_t)((uint32_t)s * (uint32_t)(SM::kStage >> 4));

@@ -26,6 +26,22 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// The same for a warp that others wait on (the MMA warp): polls without
+// sleeping first, a sleeper wakes late.
+__device__ __forceinline__ bool tc_wait_poll(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < (1 << 12); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return tc_wait(bar, parity);
+}
+
 // The same for warps that wait in every step of a pipeline: the try itself may
 // sleep (up to 1 ms) instead of coming back at once, so that waiting warps
 // leave the issue slots to the others.
