@@ -75,6 +75,7 @@ struct Kv8Attn {
   float scale;
   void* out;    // [batch][ntok][nh][hd]
   float* part;  // [2 * CTAs][irows][hd + 2]: rows of partial items, then m and l of each row
+  int4* cut;    // [items]: how the runs cut each item
   int ctas;     // of the split kernel
   int* err;
 };
@@ -106,8 +107,6 @@ __device__ __forceinline__ int entry_units(const Kv8Attn& a, int e) {
 }
 // Every thread of the CTA (128) takes entries [*e0, *e1) and gets the units
 // before them; returns all entries' units.
-// BAR: the barrier of these 128 threads.
-template <int BAR>
 __device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int* s_warp, int* before, int* e0, int* e1) {
   const int entries = a.batch * a.mgroups, per = (entries + kThreads - 1) / kThreads;
   *e0 = min(entries, tid * per);
@@ -121,7 +120,7 @@ __device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int* s_wa
     if ((tid & 31) >= o) inc += v;
   }
   if ((tid & 31) == 31) s_warp[tid >> 5] = inc;
-  asm volatile("bar.sync %0, 128;" ::"n"(BAR) : "memory");
+  __syncthreads();
   int base = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
@@ -135,6 +134,12 @@ __device__ __forceinline__ int scan_entries(const Kv8Attn& a, int tid, int* s_wa
 __device__ __forceinline__ int run_units(const Kv8Attn& a, int total) {
   return max((total + a.ctas - 1) / a.ctas, kWarps / a.nm);
 }
+
+// What the join kernel needs of item i = (b * mgroups + mg) * nkv + g: how many
+// CTAs hold a part of it (one: it is written already; 0: it has no units), the
+// first of them, and whether its part there is that CTA's first (0) or last (1)
+// partial.  Written by the CTA that begins the item.
+__device__ __forceinline__ int4 make_cut(int parts, int cta, int slot) { return make_int4(parts, cta, slot, 0); }
 
 // ------------------------------------------------------------------- fragments
 
@@ -295,12 +300,12 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
     mbar_init(&empty[tid], a.nm);
     fence_mbar_init();
   }
-  pdl_launch_dependents();
+  // (no early launch of the join kernel: its CTAs took slots of the next call's)
   pdl_wait();
 
   // this CTA's run of units
   int before, e0, e1;
-  const int total = scan_entries<1>(a, tid, s_int + 4, &before, &e0, &e1);
+  const int total = scan_entries(a, tid, s_int + 4, &before, &e0, &e1);
   const int run = run_units(a, total);
   const int u0 = (int)min((long long)blockIdx.x * run, (long long)total), u1 = min(total, u0 + run);
   if (u0 < u1)
@@ -311,6 +316,19 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         s_int[1] = u0 - before;
       }
       before += n;
+    }
+  // rows of items without a visible key are nobody's run: the CTAs share them out
+  for (int e = blockIdx.x; e < a.batch * a.mgroups; e += gridDim.x)
+    if (entry_units(a, e) == 0) {
+      const int b = e / a.mgroups, r0 = (e - b * a.mgroups) * a.irows;
+      const int n = min(a.irows, a.ntok * a.group - r0) * (HD / 4);
+      for (int i = tid; i < a.nkv * n; i += kThreads) {
+        const int g = i / n, r = r0 + i % n / (HD / 4), t = row_tok(a, r);
+        store_row4(reinterpret_cast<T*>(a.out) +
+                       (((size_t)b * a.ntok + t) * a.nh + g * a.group + (r - t * a.group)) * HD + i % (HD / 4) * 4,
+                   make_float4(0.f, 0.f, 0.f, 0.f));
+      }
+      for (int g = tid; g < a.nkv; g += kThreads) a.cut[e * a.nkv + g] = make_cut(0, 0, 0);
     }
   __syncthreads();
   if (u0 >= u1) return;
@@ -605,9 +623,10 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&empty[slot0 + use_s]);
+        if (a.nm > 1) mbar_arrive(&empty[slot0 + use_s]);
         if (mt == 0 && fill < n) {
-          if (!tc_wait_asleep(&empty[slot0 + fill_s], fill_ph ^ 1u)) atomicOr(a.err, kErrTimeout);
+          // (a warp with slots of its own has just read this one)
+          if (a.nm > 1 && !tc_wait_asleep(&empty[slot0 + fill_s], fill_ph ^ 1u)) atomicOr(a.err, kErrTimeout);
           copy_unit(fill, fill_s);
         }
       }
@@ -657,48 +676,62 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
       }
     asm volatile("bar.sync 1, 128;" ::: "memory");
     // ---- joined over the key-splitting warps: to the output, or to this CTA's
-    // first (slot 0: the item began at or before the run) or last partial
+    // first (slot 0: the item began at or before the run) or last partial.  First
+    // each row's weights, over its m and l
     const int part = 2 * blockIdx.x + (u != u0 ? 1 : 0);
     const int here = min(a.irows, rows - w.mg * a.irows);
+    if (tid < here) {
+      // row tid % kRows of warp tid / kRows; the next key part is nm warps on
+      float2 ml[kWarps];
+      float M = -INFINITY, W = 0.f;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        if (k < kw) {
+          ml[k] = *reinterpret_cast<const float2*>(MLw + 2 * (tid + kRows * a.nm * k));
+          M = fmaxf(M, ml[k].x);
+        }
+      const float ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        if (k < kw) {
+          ml[k].y = ml[k].y == 0.f ? 0.f : ml[k].y * ex2(ml[k].x - ms);
+          W += ml[k].y;
+        }
+      const float inv = W == 0.f ? 0.f : 1.f / W;
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+        if (k < kw) MLw[2 * (tid + kRows * a.nm * k)] = ml[k].y * inv;
+      if (!whole)
+        *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * a.irows * HD + 2 * ((size_t)part * a.irows + tid)) =
+            make_float2(M, W);
+    }
+    if (tid == 0 && w.at == 0)
+      a.cut[w.e * a.nkv + w.g] = make_cut((u + w.nu - 1) / run - (int)blockIdx.x + 1, blockIdx.x, u != u0 ? 1 : 0);
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll 2
     for (int i = tid; i < here * (HD / 4); i += kThreads) {
       const int rr = i / (HD / 4), d = i % (HD / 4) * 4;
-      // row rr % kRows of warp rr / kRows; the next key part is nm warps on
-      float2 ml[kWarps];
-      float4 v[kWarps];
-      float M = -INFINITY;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int k = 0; k < kWarps; ++k)
         if (k < kw) {
           const int wp = rr / kRows + k * a.nm, lr = rr % kRows;
-          ml[k] = *reinterpret_cast<const float2*>(MLw + 2 * (kRows * wp + lr));
-          v[k] = *reinterpret_cast<const float4*>(smem + (size_t)wp * SM::kShare + (lr * SM::kRowF + d) * 4);
-          M = fmaxf(M, ml[k].x);
+          const float e = MLw[2 * (kRows * wp + lr)];
+          const float4 v = *reinterpret_cast<const float4*>(smem + (size_t)wp * SM::kShare + (lr * SM::kRowF + d) * 4);
+          if (e != 0.f) {  // (a part that saw no key; NaN is kept)
+            y.x = fmaf(e, v.x, y.x);
+            y.y = fmaf(e, v.y, y.y);
+            y.z = fmaf(e, v.z, y.z);
+            y.w = fmaf(e, v.w, y.w);
+          }
         }
-      const float ms = M == -INFINITY ? 0.f : M;
-      float W = 0.f;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k)
-        if (k < kw && ml[k].y != 0.f) {
-          const float e = ml[k].y * ex2(ml[k].x - ms);
-          W += e;
-          y.x = fmaf(e, v[k].x, y.x);
-          y.y = fmaf(e, v[k].y, y.y);
-          y.z = fmaf(e, v[k].z, y.z);
-          y.w = fmaf(e, v[k].w, y.w);
-        }
-      const float inv = W == 0.f ? 0.f : 1.f / W;
-      y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
       if (whole) {
         const int r = w.mg * a.irows + rr, t = row_tok(a, r);
         store_row4(reinterpret_cast<T*>(a.out) +
                        (((size_t)w.b * a.ntok + t) * a.nh + w.g * G + (r - t * G)) * HD + d,
                    y);
       } else {
-        const size_t at = (size_t)part * a.irows + rr;
-        *reinterpret_cast<float4*>(a.part + at * HD + d) = y;
-        if (d == 0)
-          *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * a.irows * HD + 2 * at) = make_float2(M, W);
+        *reinterpret_cast<float4*>(a.part + ((size_t)part * a.irows + rr) * HD + d) = y;
       }
     }
     u += n;
@@ -711,105 +744,102 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
   }
 }
 
-// Joins the partial rows of the items that a run's end cut, in the runs' order,
-// and zeroes the rows of items without a visible key.  One CTA per row: a long
-// sequence alone on the machine has a partial row from every CTA of the split
-// kernel, so eight groups of lanes (head dim 128) read them, eight loads in
-// flight each.
+// Joins the partial rows of the items that a run's end cut, in the runs' order:
+// CTA (i, y) takes item i's rows y, y + gridDim.y, ...
+// A row is read by pg groups of lanes, eight loads in flight each: by all of the
+// CTA's groups where a few long sequences leave hundreds of parts (then the rows
+// are spread over gridDim.y), by one where a batch's items have two or three.
 constexpr int kJoinThreads = 256;
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a) {
   constexpr int kLanes = HD / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
-  constexpr int kMost = kCtasMax;  // an item's partial rows: at most one per CTA of the split kernel
-  __shared__ float s_w[kMost], s_m[kMost];
-  __shared__ int s_int[8];
-  __shared__ float s_red[8];
   __shared__ float4 s_o[kJoinThreads];
+  __shared__ float2 s_ml[kGroups];
   pdl_launch_dependents();
-  const int r = blockIdx.x, g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-  const int irows = a.irows, mg = r / irows, rr = r - mg * irows;
-  const int t = row_tok(a, r);
-  const int e = b * a.mgroups + mg;
-  int before = 0, e0 = 0, e1 = 0;
   pdl_wait();
-  int total = 0;
-  if (tid < kThreads) {
-    total = scan_entries<1>(a, tid, s_int, &before, &e0, &e1);
-    if (e0 <= e && e < e1) {
-      for (int x = e0; x < e; ++x) before += entry_units(a, x);
-      s_int[4] = before;
-      s_int[5] = total;
-    }
-  }
-  __syncthreads();
-  total = s_int[5];
-  T* out = reinterpret_cast<T*>(a.out) + (((size_t)b * a.ntok + t) * a.nh + g * a.group + (r - t * a.group)) * HD;
-  const int nu = item_units(a, seq_len(a, b), mg);
-  const int lane = tid % kLanes, grp = tid / kLanes;
-  if (nu == 0) {
-    if (grp == 0) store_row4(out + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f));
-    return;
-  }
-  const int run = run_units(a, total), us = s_int[4] + g * nu;
-  const int c0 = us / run, n = (us + nu - 1) / run - c0 + 1;
-  if (n == 1) return;  // the split kernel has written it
-  // partial row i: of CTA c0 + i, its first partial unless the item began inside its run
-  const size_t at0 = ((size_t)2 * c0 + (us > c0 * run ? 1 : 0)) * irows + rr;
-  const size_t at1 = (size_t)2 * c0 * irows + rr, step = (size_t)2 * irows;
+  const int tid = threadIdx.x, lane = tid % kLanes, grp = tid / kLanes;
+  const int4 cut = a.cut[blockIdx.x];
+  const int n = cut.x, c = cut.y;
+  if (n < 2) return;
+  const int e = blockIdx.x / a.nkv, g = blockIdx.x - e * a.nkv, b = e / a.mgroups, mg = e - b * a.mgroups;
+  const int irows = a.irows;
+  const int here = min(irows, a.ntok * a.group - mg * irows);
+  int pg = kGroups;
+  if (gridDim.y == 1)
+    while (pg > 1 && (kGroups / pg < here || pg > n)) pg >>= 1;
+  const int per = kGroups / pg;              // rows of a pass
+  const int sub = grp % pg, row = grp / pg;  // this group's share of the parts, its row of the pass
   const float* ml = a.part + (size_t)2 * a.ctas * irows * HD;
-  float M = -INFINITY;
-  for (int i = tid; i < n; i += kJoinThreads) {
-    const float2 v = *reinterpret_cast<const float2*>(ml + 2 * (i == 0 ? at0 : at1 + i * step));
-    s_m[i] = v.x;
-    s_w[i] = v.y;
-    M = fmaxf(M, v.x);
-  }
-  // the first loads of the rows do not wait for the weights
-  float4 v[kBatch];
-  auto load = [&](int i0) {
+  for (int base = blockIdx.y; base < here; base += gridDim.y == 1 ? per : (int)gridDim.y) {
+    const int rr = gridDim.y == 1 ? base + row : base;
+    const bool in = rr < here;
+    // part i: of CTA c + i, its first partial (CTA c's as the cut says)
+    const size_t at0 = ((size_t)2 * c + cut.z) * irows + rr;
+    const size_t at1 = (size_t)2 * c * irows + rr, step = (size_t)2 * irows;
+    float M = -INFINITY, W = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = sub; in && i0 < n; i0 += kBatch * pg) {
+      float4 v[kBatch];
+      float2 w[kBatch];
+      float mb = M;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * kGroups;
-      v[k] = i < n ? *reinterpret_cast<const float4*>(a.part + (i == 0 ? at0 : at1 + i * step) * HD + 4 * lane)
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  };
-  load(grp);
-  M = warp_max(M);
-  if ((tid & 31) == 0) s_red[tid >> 5] = M;
-  __syncthreads();
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * pg;
+        const size_t at = i == 0 ? at0 : at1 + i * step;
+        if (i < n) {
+          w[k] = *reinterpret_cast<const float2*>(ml + 2 * at);
+          v[k] = *reinterpret_cast<const float4*>(a.part + at * HD + 4 * lane);
+        }
+      }
 #pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, s_red[k]);
-  const float ms = M == -INFINITY ? 0.f : M;
-  for (int i = tid; i < n; i += kJoinThreads) s_w[i] = s_w[i] == 0.f ? 0.f : s_w[i] * ex2(s_m[i] - ms);
-  __syncthreads();
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  float W = 0.f;
-  for (int i0 = grp; i0 < n; i0 += kBatch * kGroups) {
-    if (i0 != grp) load(i0);
+      for (int k = 0; k < kBatch; ++k)
+        if (i0 + k * pg < n) mb = fmaxf(mb, w[k].x);
+      const float ms = mb == -INFINITY ? 0.f : mb;
+      const float keep = ex2(M - ms);
+      M = mb;
+      W *= keep;
+      y = make_float4(y.x * keep, y.y * keep, y.z * keep, y.w * keep);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * kGroups;
-      const float x = i < n ? s_w[i] : 0.f;
-      if (x == 0.f) continue;  // (a row that saw no key there; NaN is kept)
-      W += x;
-      y.x = fmaf(x, v[k].x, y.x);
-      y.y = fmaf(x, v[k].y, y.y);
-      y.z = fmaf(x, v[k].z, y.z);
-      y.w = fmaf(x, v[k].w, y.w);
+      for (int k = 0; k < kBatch; ++k)
+        if (i0 + k * pg < n && w[k].y != 0.f) {  // (a part that saw no key; NaN is kept)
+          const float e = w[k].y * ex2(w[k].x - ms);
+          W += e;
+          y.x = fmaf(e, v[k].x, y.x);
+          y.y = fmaf(e, v[k].y, y.y);
+          y.z = fmaf(e, v[k].z, y.z);
+          y.w = fmaf(e, v[k].w, y.w);
+        }
     }
-  }
-  s_o[tid] = y;
-  if (lane == 0) s_m[grp] = W;  // (s_m is read no more)
-  __syncthreads();
-  if (grp == 0) {
-    for (int k = 1; k < kGroups; ++k) {
-      const float4 u = s_o[k * kLanes + lane];
-      y = make_float4(y.x + u.x, y.y + u.y, y.z + u.z, y.w + u.w);
-      W += s_m[k];
+    if (pg > 1) {  // the groups of a row, in order
+      __syncthreads();
+      s_o[tid] = y;
+      if (lane == 0) s_ml[grp] = make_float2(M, W);
+      __syncthreads();
+      if (sub == 0) {
+        for (int k = 1; k < pg; ++k) M = fmaxf(M, s_ml[grp + k].x);
+        const float ms = M == -INFINITY ? 0.f : M;
+        y = make_float4(0.f, 0.f, 0.f, 0.f);
+        W = 0.f;
+        for (int k = 0; k < pg; ++k) {
+          const float2 u = s_ml[grp + k];
+          if (u.y == 0.f) continue;
+          const float e = ex2(u.x - ms);
+          const float4 v = s_o[tid + k * kLanes];
+          W = fmaf(e, u.y, W);
+          y.x = fmaf(e, v.x, y.x);
+          y.y = fmaf(e, v.y, y.y);
+          y.z = fmaf(e, v.z, y.z);
+          y.w = fmaf(e, v.w, y.w);
+        }
+      }
     }
-    const float inv = W == 0.f ? 0.f : 1.f / W;
-    store_row4(out + 4 * lane, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    if (in && sub == 0) {
+      const float inv = W == 0.f ? 0.f : 1.f / W;
+      const int r = mg * irows + rr, t = row_tok(a, r);
+      store_row4(reinterpret_cast<T*>(a.out) +
+                     (((size_t)b * a.ntok + t) * a.nh + g * a.group + (r - t * a.group)) * HD + 4 * lane,
+                 make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    }
   }
 }
 
@@ -827,7 +857,9 @@ q2_status split_t(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaSt
   Q2_TRY(make_tmap_2d_u8(&km, kc, rows, HD, HD, kKeys, HD, HD));
   Q2_TRY(make_tmap_2d_u8(&vm, vc, rows, HD, HD, kKeys, HD, HD));
   Q2_LAUNCH(kernel, dim3(a.ctas), dim3(kThreads), SM::kTotal, st, true, a, km, vm);
-  Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(a.ntok * a.group, a.nkv, a.batch), dim3(kJoinThreads), 0, st, true, a);
+  // few items: a CTA per row of each, else one per item
+  const int items = a.batch * a.nkv * a.mgroups;
+  Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(items, items <= 32 ? a.irows : 1), dim3(kJoinThreads), 0, st, true, a);
   return Q2_OK;
 }
 
@@ -847,9 +879,9 @@ q2_status split(const Kv8Attn& a, int hd, const uint8_t* kc, const uint8_t* vc, 
 // the split kernel.
 struct SplitPlan {
   int nt, nm, irows, mgroups, ctas;
-  size_t bytes;
+  size_t cut_bytes, bytes;
 };
-SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd) {
+SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd) {
   SplitPlan p;
   const int rows = (int)(ntok * (nh / nkv));
   p.nt = rows > 8 ? 2 : 1;
@@ -859,7 +891,8 @@ SplitPlan split_plan(size_t ntok, size_t nh, size_t nkv, size_t hd) {
   p.mgroups = ceil_div(rows, p.irows);
   p.ctas = num_sms() * (p.nt == 1 ? 3 : 2);  // all resident at once
   if (p.ctas > kCtasMax) p.ctas = kCtasMax;
-  p.bytes = (size_t)2 * p.ctas * p.irows * (hd + 2) * sizeof(float);
+  p.cut_bytes = (batch * p.mgroups * nkv * sizeof(int4) + 255) / 256 * 256;
+  p.bytes = p.cut_bytes + (size_t)2 * p.ctas * p.irows * (hd + 2) * sizeof(float);
   return p;
 }
 
@@ -940,7 +973,7 @@ q2_status attn_tc(const Kv8Attn& a, const void* kc, const void* vc, void* ws, si
 
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
                cudaStream_t st) {
-  const SplitPlan p = split_plan(a.ntok, a.nh, a.nkv, hd);
+  const SplitPlan p = split_plan(a.batch, a.ntok, a.nh, a.nkv, hd);
   Q2_TRY(check_workspace(ws, ws_bytes, p.bytes));
   if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 29)) {
     set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^29");
@@ -953,7 +986,8 @@ q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, voi
   a.irows = p.irows;
   a.mgroups = p.mgroups;
   a.ctas = p.ctas;
-  a.part = static_cast<float*>(ws);
+  a.cut = static_cast<int4*>(ws);
+  a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.cut_bytes);
   const auto* k = static_cast<const uint8_t*>(kc);
   const auto* v = static_cast<const uint8_t*>(vc);
   return dtype == Q2_BF16 ? split<__nv_bfloat16>(a, hd, k, v, st) : split<float>(a, hd, k, v, st);
@@ -1064,7 +1098,7 @@ q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len
                "kv8_attention_workspace: with a total_len, batch must be 1 and ntok at most total_len");
   *bytes = 0;
   if (batch == 0 || ntok == 0) return Q2_OK;
-  *bytes = split_plan(ntok, nh, nkv, hd).bytes;
+  *bytes = split_plan(batch, ntok, nh, nkv, hd).bytes;
   if (total_len && use_tc(ntok, nh / nkv, hd, dtype)) {
     const size_t tc = tc_plan(ntok, total_len, nh, nkv).bytes;
     if (tc > *bytes) *bytes = tc;  // (either path, as the alignment of q and out has it)

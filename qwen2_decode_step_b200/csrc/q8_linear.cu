@@ -37,6 +37,10 @@
 // word and the kernel carries on to its end.
 #include <cooperative_groups.h>
 
+#include <map>
+#include <mutex>
+#include <tuple>
+
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "tcgen05.cuh"
@@ -513,6 +517,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// How many clusters of cs CTAs of `kernel` the current device runs at once; asked
+// once per kernel, size and device.
+q2_status active_clusters(const void* kernel, int cs, size_t smem, int* n) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void*, int>, int> known;
+  int dev = 0;
+  Q2_CUDA_TRY(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lk(mu);
+  const auto key = std::make_tuple(dev, kernel, cs);
+  const auto it = known.find(key);
+  if (it != known.end()) {
+    *n = it->second;
+    return Q2_OK;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  Q2_CUDA_TRY(cudaOccupancyMaxActiveClusters(n, kernel, &cfg));
+  known[key] = *n;
+  return Q2_OK;
+}
+
 template <typename T, bool WIDE, int BN, int STAGES>
 q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t st) {
   using SM = Q8Smem<WIDE, BN, STAGES>;
@@ -537,12 +571,26 @@ q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t
     return Q2_ERR_SHAPE;
   }
   a.tiles = (int)tiles;
+  // CTAs per tile.  Time in groups: a wave of tiles takes its groups and about
+  // kFixed more (start, last store); joining a split tile about kJoin.  Clusters
+  // pack badly (3 CTAs each: 48 clusters of 144 CTAs did not fit 148 SMs at once
+  // and 512 x 1536 x 8960 took two waves, 26 us), so the driver is asked how many
+  // are resident together.
+  constexpr int kFixed = 4, kJoin = 3;
   const int sms = num_sms();
-  // CTAs per tile: as many as leave no SM without work, each with a group
-  int cs = tiles < sms ? (int)(sms / tiles) : 1;
-  cs = cs > kClusterMax ? kClusterMax : cs;
-  cs = cs > a.groups ? a.groups : cs;
-  a.g_per = (a.groups + cs - 1) / cs;
+  int best = 1;
+  long long best_cost = (tiles + sms - 1) / sms * (a.groups + kFixed);
+  for (int cs = 2; cs <= kClusterMax && cs <= a.groups && tiles * cs <= sms; ++cs) {
+    int active = 0;
+    Q2_TRY(active_clusters(reinterpret_cast<const void*>(kernel), cs, SM::kTotal, &active));
+    if (active < 1) continue;
+    const long long cost = (tiles + active - 1) / active * ((a.groups + cs - 1) / cs + kFixed) + kJoin;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = cs;
+    }
+  }
+  a.g_per = (a.groups + best - 1) / best;
   a.csize = (a.groups + a.g_per - 1) / a.g_per;  // every CTA has a group
   CUtensorMap tx, tw;
   Q2_TRY(make_tmap_2d_u8(&tx, xq, (uint64_t)a.M, (uint64_t)K, (uint64_t)K, WIDE ? kLanes : BN, kGroup, 128));
