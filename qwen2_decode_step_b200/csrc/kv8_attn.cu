@@ -26,9 +26,12 @@
 //           the A operand.  P turns from the scores' layout by movmatrix.
 // The query rows are scaled by a power of two into fp16's range (exact for
 // bf16; fp32 queries are split into a high and a low fp16 part, two MMAs, and
-// so are their probabilities).  Softmax in fp32, online, with p = 2^(s - m + 14):
-// the common factor cancels and keeps probabilities down to 2^-28 of the
-// largest at fp16's full 11 bits.  The scale of K multiplies the scores; the
+// so are their probabilities).  Softmax in fp32, online, with p = 2^(s - m + 6),
+// m the row's reference: the largest score when it was last taken.  It is taken
+// again (shuffles over the eight lanes that hold a row's keys, the output
+// rescaled) only when a score passes it by 8, so that most units need one vote;
+// the common factor cancels, p stays below 2^14 and probabilities down to 2^-20
+// of the largest keep fp16's full 11 bits.  The scale of K multiplies the scores; the
 // output is accumulated in units of the current block's V scale and moved to
 // the next block's where that differs (a power of two: exact).
 //
@@ -56,7 +59,7 @@ constexpr int kKeys = 32;                       // keys per unit
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasMax = 512;
-constexpr float kPBias = 14.f;                  // p <= 2^14 in fp16
+constexpr float kPBias = 6.f, kGrow = 8.f;      // p <= 2^(6 + 8) in fp16, see softmax
 
 struct Kv8Attn {
   const void* q;
@@ -68,7 +71,7 @@ struct Kv8Attn {
   int batch, ntok, nh, nkv, max_seq, nblk;
   int group;      // nh / nkv
   unsigned magic; // ceil(2^32 / group): r / group = umulhi(r, magic) for group > 1
-  int nt;       // 8-row tiles of a warp: 1 or 2
+  int nt;       // 8-row tiles of a warp: 1, 2 or 4
   int nm;       // warps that share an item's rows: 1, 2 or 4
   int irows;    // rows of an item: 8 nt nm
   int mgroups;  // items of a (sequence, kv head)
@@ -210,15 +213,19 @@ template <int HD, int NT>
 struct SplitSmem {
   // slots per warp: with one row tile three CTAs fit an SM, with two (twice the
   // accumulators) two
-  static constexpr int kDepth = NT == 1 ? 2 : 3;
+  static constexpr int kDepth = NT == 2 ? 3 : 2;
   static constexpr int kCtas = NT == 1 ? 3 : 2;
+  // with four the query fragments stay in shared memory, each lane its own: [tile][word][lane][2]
+  static constexpr bool kQShared = NT == 4;
+  static constexpr size_t kQWarp = kQShared ? (size_t)NT * (HD / 16) * 32 * 8 : 0;
   static constexpr size_t kTile = (size_t)kKeys * HD;
   static constexpr size_t kSlot = 2 * kTile;
   // a warp's rows at an item's end, over its share of the slots (free then);
   // rows 4 floats longer against conflicts
   static constexpr int kRows = 8 * NT, kRowF = HD + 4;
   static constexpr size_t kShare = kDepth * kSlot > (size_t)kRows * kRowF * 4 ? kDepth * kSlot : (kRows * kRowF * 4 + 1023) / 1024 * 1024;
-  static constexpr size_t kML = kWarps * kShare;
+  static constexpr size_t kQ = kWarps * kShare;
+  static constexpr size_t kML = kQ + kWarps * kQWarp;
   static constexpr size_t kNan = kML + (size_t)kWarps * kRows * 2 * 4;  // per warp: first NaN position of each dim
   static constexpr size_t kBars = kNan + (size_t)kWarps * HD * 4;
   static constexpr size_t kInts = kBars + 2 * kWarps * kDepth * 8;
@@ -414,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
     int fill = kg + early * kw;
 
     // query fragments (the B operand: row gq, the lane's dims in words of four)
-    uint32_t qb[kTerms][NT][kW][2];
+    uint32_t qb[kTerms][SM::kQShared ? 1 : NT][kW][2];
+    uint2* qsh = reinterpret_cast<uint2*>(smem + SM::kQ + warp * SM::kQWarp) + lane;  // [NT][kW][32]
     float sc[NT][2];   // of rows 2 tq and 2 tq + 1 of each tile, as the scores sit
     int lim[NT][2];
 #pragma unroll
@@ -434,12 +442,18 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
 #pragma unroll
       for (int j = 0; j < kW; ++j) {
         const float x0 = f[4 * j] * up, x1 = f[4 * j + 1] * up, x2 = f[4 * j + 2] * up, x3 = f[4 * j + 3] * up;
-        qb[0][h][j][0] = pack_f16x2(x0, x1);
-        qb[0][h][j][1] = pack_f16x2(x2, x3);
-        if constexpr (kWide) {
-          const float2 y0 = unpack_f16x2(qb[0][h][j][0]), y1 = unpack_f16x2(qb[0][h][j][1]);
-          qb[1][h][j][0] = pack_f16x2(x0 - y0.x, x1 - y0.y);
-          qb[1][h][j][1] = pack_f16x2(x2 - y1.x, x3 - y1.y);
+        const uint32_t q0 = pack_f16x2(x0, x1), q1 = pack_f16x2(x2, x3);
+        if constexpr (SM::kQShared) {
+          static_assert(!SM::kQShared || !kWide, "four row tiles: one term");
+          qsh[(h * kW + j) * 32] = make_uint2(q0, q1);
+        } else {
+          qb[0][h][j][0] = q0;
+          qb[0][h][j][1] = q1;
+          if constexpr (kWide) {
+            const float2 y0 = unpack_f16x2(q0), y1 = unpack_f16x2(q1);
+            qb[1][h][j][0] = pack_f16x2(x0 - y0.x, x1 - y0.y);
+            qb[1][h][j][1] = pack_f16x2(x2 - y1.x, x3 - y1.y);
+          }
         }
       }
 #pragma unroll
@@ -477,37 +491,77 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
       if (m0 < rows) {  // (three warps' rows of four: the last has none)
         // ---- scores: the key tiles side by side, so that no MMA waits for the last
         float s[NT][kMt][4];
-        uint32_t kb[kMt][2][kW];
-#pragma unroll
-        for (int m = 0; m < kMt; ++m)
+        auto load_keys = [&](int m, uint32_t (*kb)[kW]) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r = 16 * m + 8 * i + gq;
             if constexpr (HD == 128) {
-              lds_words<16>(kt + tile_off<HD>(r, 2 * tq), kb[m][i]);
-              lds_words<16>(kt + tile_off<HD>(r, 2 * tq + 1), kb[m][i] + 4);
+              lds_words<16>(kt + tile_off<HD>(r, 2 * tq), kb[i]);
+              lds_words<16>(kt + tile_off<HD>(r, 2 * tq + 1), kb[i] + 4);
             } else if constexpr (HD == 64) {
-              lds_words<16>(kt + tile_off<HD>(r, tq), kb[m][i]);
+              lds_words<16>(kt + tile_off<HD>(r, tq), kb[i]);
             } else {
-              lds_words<8>(kt + tile_off<HD>(r, tq >> 1) + 8 * (tq & 1), kb[m][i]);
+              lds_words<8>(kt + tile_off<HD>(r, tq >> 1) + 8 * (tq & 1), kb[i]);
             }
           }
+        };
+        auto convert = [](const uint32_t (*kb)[kW], int j, uint32_t* ka) {
+          ka[0] = e4m3x2_to_f16x2((uint16_t)(kb[0][j] & 0xffffu));
+          ka[1] = e4m3x2_to_f16x2((uint16_t)(kb[1][j] & 0xffffu));
+          ka[2] = e4m3x2_to_f16x2((uint16_t)(kb[0][j] >> 16));
+          ka[3] = e4m3x2_to_f16x2((uint16_t)(kb[1][j] >> 16));
+        };
 #pragma unroll
         for (int h = 0; h < NT; ++h)
 #pragma unroll
           for (int m = 0; m < kMt; ++m) s[h][m][0] = s[h][m][1] = s[h][m][2] = s[h][m][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < kW; ++j)
+        if constexpr (SM::kQShared) {  // the row tiles are side by side: one key tile at a time
 #pragma unroll
           for (int m = 0; m < kMt; ++m) {
-            const uint32_t ka[4] = {
-                e4m3x2_to_f16x2((uint16_t)(kb[m][0][j] & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(kb[m][1][j] & 0xffffu)),
-                e4m3x2_to_f16x2((uint16_t)(kb[m][0][j] >> 16)), e4m3x2_to_f16x2((uint16_t)(kb[m][1][j] >> 16))};
+            uint32_t kb[2][kW];
+            load_keys(m, kb);
 #pragma unroll
-            for (int h = 0; h < NT; ++h)
+            for (int j = 0; j < kW; ++j) {
+              uint32_t ka[4];
+              convert(kb, j, ka);
 #pragma unroll
-              for (int e = 0; e < kTerms; ++e) mma_f16(s[h][m], ka, qb[e][h][j][0], qb[e][h][j][1]);
+              for (int h = 0; h < NT; ++h) {
+                const uint2 q = qsh[(h * kW + j) * 32];
+                mma_f16(s[h][m], ka, q.x, q.y);
+              }
+            }
           }
+        } else {
+          // with one row tile and one term two chains of sums per key tile, added
+          // at the end: a chain of eight MMAs waits for itself
+          constexpr int kChains = NT * kTerms == 1 ? 2 : 1;
+          float s2[kChains == 2 ? kMt : 1][4];
+          uint32_t kb[kMt][2][kW];
+#pragma unroll
+          for (int m = 0; m < kMt; ++m) load_keys(m, kb[m]);
+          if constexpr (kChains == 2) {
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) s2[m][0] = s2[m][1] = s2[m][2] = s2[m][3] = 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < kW; ++j)
+#pragma unroll
+            for (int m = 0; m < kMt; ++m) {
+              uint32_t ka[4];
+              convert(kb[m], j, ka);
+#pragma unroll
+              for (int h = 0; h < NT; ++h)
+#pragma unroll
+                for (int e = 0; e < kTerms; ++e)
+                  mma_f16(kChains == 2 && j % 2 ? s2[m] : s[h][m], ka, qb[e][h][j][0], qb[e][h][j][1]);
+            }
+          if constexpr (kChains == 2) {
+#pragma unroll
+            for (int m = 0; m < kMt; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[0][m][i] += s2[m][i];
+          }
+        }
         // ---- the unit of this block's V scale (never 2^60 below the largest so
         // far: the output in units of it stays in range)
         unit_max = fmaxf(unit_max, vsc);
@@ -515,17 +569,41 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         const float ratio = unit_new == unit ? 1.f : unit / unit_new;
         const float pf = vsc == unit_new ? 1.f : vsc / unit_new;
         unit = unit_new;
-        // ---- softmax: value 2 i + j of tile m is key 16 m + 8 i + gq, row 2 tq + j
         const bool edge = key0 + kKeys > clear;
-        uint32_t pb[kTerms][NT][kMt][2];
-        float move[NT][2];  // of the output: to the new maximum and unit
-        bool moved = false;
+        // ---- rows past the sequence, NaN that not every row sees
+        bool drop_nan = false;
+        if (edge && (a.ntok > 1 || key0 + kKeys > w.len)) {
+          if (!some_nan) {
+            for (int d = lane; d < HD; d += 32) first_nan[d] = INT32_MAX;
+            __syncwarp();
+          }
+          drop_nan = prepare_edge<HD>(tile + SM::kTile, w.len - key0, a.ntok > 1, key0, first_nan, lane);
+          some_nan |= drop_nan;
+          __syncwarp();
+        }
+        // ---- V of the first 16 keys, on its way while the softmax runs
+        auto load_values = [&](int kk, uint32_t (*r)[4]) {
 #pragma unroll
-        for (int h = 0; h < NT; ++h) {
+          for (int c2 = 0; c2 < kC / 2; ++c2)
+            ldsm4_t(vt + tile_off<HD>(16 * kk + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)), r[c2]);
+          if (drop_nan) {
+#pragma unroll
+            for (int c2 = 0; c2 < kC / 2; ++c2)
+#pragma unroll
+              for (int z = 0; z < 4; ++z) r[c2][z] &= ~nan_bytes(r[c2][z]);
+          }
+        };
+        uint32_t r[kC / 2][4];
+        load_values(0, r);
+        // ---- softmax: value 2 i + j of tile m is key 16 m + 8 i + gq, row 2 tq + j
+        bool grow = false;
+        float top[NT][2];
+#pragma unroll
+        for (int h = 0; h < NT; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float f = sc[h][j] * ksc;
-            float mx = -INFINITY;
+            top[h][j] = -INFINITY;
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
 #pragma unroll
@@ -533,27 +611,58 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
                 float v = s[h][m][2 * i + j] * f;
                 if (edge && key0 + 16 * m + 8 * i + gq >= lim[h][j]) v = -INFINITY;
                 s[h][m][2 * i + j] = v;
-                mx = fmaxf(mx, v);
+                top[h][j] = fmaxf(top[h][j], v);
               }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m_run[h][j], mx);
-            const float ms = mn == -INFINITY ? 0.f : mn;
-            const float alpha = ex2(m_run[h][j] - ms);
-            move[h][j] = ratio * alpha;
-            moved |= move[h][j] != 1.f;
-            m_run[h][j] = mn;
+            grow |= top[h][j] > m_run[h][j] + kGrow;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+          float move[NT][2];  // of the output: to the new reference and unit
+#pragma unroll
+          for (int o2 = 4; o2 < 32; o2 <<= 1)
+#pragma unroll
+            for (int h = 0; h < NT; ++h)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) top[h][j] = fmaxf(top[h][j], __shfl_xor_sync(0xffffffffu, top[h][j], o2));
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float mn = fmaxf(m_run[h][j], top[h][j]);
+              const float alpha = ex2(m_run[h][j] - (mn == -INFINITY ? 0.f : mn));
+              move[h][j] = ratio * alpha;
+              l_run[h][j] *= alpha;
+              m_run[h][j] = mn;
+            }
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[h][c][j] *= move[h][j & 1];
+        } else if (ratio != 1.f) {
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[h][c][j] *= ratio;
+        }
+        uint32_t pb[kTerms][NT][kMt][2];
+#pragma unroll
+        for (int h = 0; h < NT; ++h) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float ms = (m_run[h][j] == -INFINITY ? 0.f : m_run[h][j]) - kPBias;
             float sum = 0.f;
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float p = ex2(s[h][m][2 * i + j] - ms + kPBias);
+                const float p = ex2(s[h][m][2 * i + j] - ms);
                 s[h][m][2 * i + j] = p;
                 sum += p;
               }
-            l_run[h][j] = l_run[h][j] * alpha + sum;
+            l_run[h][j] += sum;
           }
           if (pf != 1.f) {
 #pragma unroll
@@ -574,38 +683,10 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
               }
             }
         }
-        if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-          for (int h = 0; h < NT; ++h)
-#pragma unroll
-            for (int c = 0; c < kC; ++c)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[h][c][j] *= move[h][j & 1];
-        }
-        // ---- rows past the sequence, NaN that not every row sees
-        bool drop_nan = false;
-        if (edge && (a.ntok > 1 || key0 + kKeys > w.len)) {
-          if (!some_nan) {
-            for (int d = lane; d < HD; d += 32) first_nan[d] = INT32_MAX;
-            __syncwarp();
-          }
-          drop_nan = prepare_edge<HD>(tile + SM::kTile, w.len - key0, a.ntok > 1, key0, first_nan, lane);
-          some_nan |= drop_nan;
-          __syncwarp();
-        }
         // ---- output
 #pragma unroll
         for (int kk = 0; kk < kMt; ++kk) {
-          uint32_t r[kC / 2][4];
-#pragma unroll
-          for (int c2 = 0; c2 < kC / 2; ++c2)
-            ldsm4_t(vt + tile_off<HD>(16 * kk + (mi & 1) * 8 + mr, 2 * c2 + (mi >> 1)), r[c2]);
-          if (drop_nan) {
-#pragma unroll
-            for (int c2 = 0; c2 < kC / 2; ++c2)
-#pragma unroll
-              for (int z = 0; z < 4; ++z) r[c2][z] &= ~nan_bytes(r[c2][z]);
-          }
+          if (kk > 0) load_values(kk, r);
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
             // bytes (key, dim): (0, even), (0, odd), (1, even), (1, odd)
@@ -863,15 +944,19 @@ q2_status split_t(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaSt
   return Q2_OK;
 }
 
+template <typename T, int HD>
+q2_status split_hd(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2)
+    if (a.nt == 4) return split_t<T, HD, 4>(a, kc, vc, st);
+  return a.nt == 1 ? split_t<T, HD, 1>(a, kc, vc, st) : split_t<T, HD, 2>(a, kc, vc, st);
+}
+
 template <typename T>
 q2_status split(const Kv8Attn& a, int hd, const uint8_t* kc, const uint8_t* vc, cudaStream_t st) {
-  switch (2 * hd + a.nt) {
-    case 65: return split_t<T, 32, 1>(a, kc, vc, st);
-    case 66: return split_t<T, 32, 2>(a, kc, vc, st);
-    case 129: return split_t<T, 64, 1>(a, kc, vc, st);
-    case 130: return split_t<T, 64, 2>(a, kc, vc, st);
-    case 257: return split_t<T, 128, 1>(a, kc, vc, st);
-    default: return split_t<T, 128, 2>(a, kc, vc, st);
+  switch (hd) {
+    case 32: return split_hd<T, 32>(a, kc, vc, st);
+    case 64: return split_hd<T, 64>(a, kc, vc, st);
+    default: return split_hd<T, 128>(a, kc, vc, st);
   }
 }
 
@@ -881,10 +966,14 @@ struct SplitPlan {
   int nt, nm, irows, mgroups, ctas;
   size_t cut_bytes, bytes;
 };
-SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd) {
+SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd, int dtype) {
   SplitPlan p;
   const int rows = (int)(ntok * (nh / nkv));
-  p.nt = rows > 8 ? 2 : 1;
+  // Four tiles convert K and V half as often as two, but leave a warp alone with
+  // them: 30 rows (4 sequences of up to 20011 positions) 26 us with two, 30 with
+  // four; 384 rows over 32768 positions 100 and 82.  (fp32's second terms leave no
+  // registers for four.)
+  p.nt = rows <= 8 ? 1 : rows <= 64 || dtype == Q2_F32 ? 2 : 4;
   const int warps = ceil_div(rows, 8 * p.nt);
   p.nm = warps > 2 ? 4 : warps;
   p.irows = 8 * p.nt * p.nm;
@@ -908,8 +997,8 @@ q2_status check_workspace(const void* ws, size_t have, size_t need) {
 // The tcgen05 attention takes 128 rows of one query head a tile, whether they
 // exist or not, and the copy of K and V comes before it; the split kernel's time
 // goes with the rows of a kv head.  12 / 2 heads over 32768 keys: 64 prompt
-// tokens (384 rows) 100 us here against 115 there, 128 (768 rows) 176 against
-// 115; over 4096 keys 128 tokens 52 against 62, 4 / 4 heads 64 tokens 25 against 62.
+// tokens (384 rows) 82 us in the split kernel against 115, 128 (768 rows) 141
+// against 112; 512 tokens over 512 keys 48 against 24.
 constexpr int kTcRows = 512;
 bool use_tc(size_t ntok, size_t group, size_t hd, int dtype) {
   return dtype == Q2_BF16 && hd == 128 && ntok >= 16 && ntok * group >= kTcRows;
@@ -973,7 +1062,7 @@ q2_status attn_tc(const Kv8Attn& a, const void* kc, const void* vc, void* ws, si
 
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
                cudaStream_t st) {
-  const SplitPlan p = split_plan(a.batch, a.ntok, a.nh, a.nkv, hd);
+  const SplitPlan p = split_plan(a.batch, a.ntok, a.nh, a.nkv, hd, dtype);
   Q2_TRY(check_workspace(ws, ws_bytes, p.bytes));
   if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 29)) {
     set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^29");
@@ -1098,7 +1187,7 @@ q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len
                "kv8_attention_workspace: with a total_len, batch must be 1 and ntok at most total_len");
   *bytes = 0;
   if (batch == 0 || ntok == 0) return Q2_OK;
-  *bytes = split_plan(batch, ntok, nh, nkv, hd).bytes;
+  *bytes = split_plan(batch, ntok, nh, nkv, hd, dtype).bytes;
   if (total_len && use_tc(ntok, nh / nkv, hd, dtype)) {
     const size_t tc = tc_plan(ntok, total_len, nh, nkv).bytes;
     if (tc > *bytes) *bytes = tc;  // (either path, as the alignment of q and out has it)
