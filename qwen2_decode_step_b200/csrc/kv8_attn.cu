@@ -80,6 +80,7 @@ struct Kv8Attn {
   float* part;  // [2 * CTAs][irows][hd + 2]: rows of partial items, then m and l of each row
   int4* cut;    // [items]: how the runs cut each item
   int ctas;     // of the split kernel
+  int whole;    // a CTA per item, nothing is cut (see whole_items)
   int* err;
 };
 
@@ -286,6 +287,18 @@ __device__ __noinline__ bool prepare_edge(uint8_t* vt, int stale, bool look, int
   return __any_sync(0xffffffffu, any);
 }
 
+// Zeroes an m-group's rows of kv heads [g0, g1).
+template <typename T, int HD>
+__device__ __noinline__ void zero_rows(const Kv8Attn& a, int b, int mg, int g0, int g1, int tid) {
+  const int r0 = mg * a.irows, n = min(a.irows, a.ntok * a.group - r0) * (HD / 4);
+  for (int i = tid; i < (g1 - g0) * n; i += kThreads) {
+    const int g = g0 + i / n, r = r0 + i % n / (HD / 4), t = row_tok(a, r);
+    store_row4(reinterpret_cast<T*>(a.out) +
+                   (((size_t)b * a.ntok + t) * a.nh + g * a.group + (r - t * a.group)) * HD + i % (HD / 4) * 4,
+               make_float4(0.f, 0.f, 0.f, 0.f));
+  }
+}
+
 template <typename T, int HD, int NT>
 __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
     kv8_split_kernel(const Kv8Attn a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -311,36 +324,44 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
   pdl_wait();
 
   // this CTA's run of units
-  int before, e0, e1;
-  const int total = scan_entries(a, tid, s_int + 4, &before, &e0, &e1);
-  const int run = run_units(a, total);
-  const int u0 = (int)min((long long)blockIdx.x * run, (long long)total), u1 = min(total, u0 + run);
-  if (u0 < u1)
-    for (int e = e0; e < e1; ++e) {
-      const int n = entry_units(a, e);
-      if (before <= u0 && u0 < before + n) {
-        s_int[0] = e;
-        s_int[1] = u0 - before;
-      }
-      before += n;
-    }
-  // rows of items without a visible key are nobody's run: the CTAs share them out
-  for (int e = blockIdx.x; e < a.batch * a.mgroups; e += gridDim.x)
-    if (entry_units(a, e) == 0) {
-      const int b = e / a.mgroups, r0 = (e - b * a.mgroups) * a.irows;
-      const int n = min(a.irows, a.ntok * a.group - r0) * (HD / 4);
-      for (int i = tid; i < a.nkv * n; i += kThreads) {
-        const int g = i / n, r = r0 + i % n / (HD / 4), t = row_tok(a, r);
-        store_row4(reinterpret_cast<T*>(a.out) +
-                       (((size_t)b * a.ntok + t) * a.nh + g * a.group + (r - t * a.group)) * HD + i % (HD / 4) * 4,
-                   make_float4(0.f, 0.f, 0.f, 0.f));
-      }
-      for (int g = tid; g < a.nkv; g += kThreads) a.cut[e * a.nkv + g] = make_cut(0, 0, 0);
-    }
-  __syncthreads();
-  if (u0 >= u1) return;
   UnitWalk w;
-  w.seek(a, s_int[0], s_int[1]);
+  int u0 = 0, u1 = 0, run = 1;
+  if (a.whole) {
+    const int e = blockIdx.x / a.nkv;
+    w.e = e;
+    w.entry_of(a);
+    w.g = blockIdx.x - e * a.nkv;
+    w.at = 0;
+    u1 = w.nu;
+    if (w.nu == 0) zero_rows<T, HD>(a, w.b, w.mg, w.g, w.g + 1, tid);
+    __syncthreads();  // the barriers are set up
+    if (w.nu == 0) return;
+  } else {
+    int before, e0, e1;
+    const int total = scan_entries(a, tid, s_int + 4, &before, &e0, &e1);
+    run = run_units(a, total);
+    u0 = (int)min((long long)blockIdx.x * run, (long long)total);
+    u1 = min(total, u0 + run);
+    if (u0 < u1)
+      for (int e = e0; e < e1; ++e) {
+        const int n = entry_units(a, e);
+        if (before <= u0 && u0 < before + n) {
+          s_int[0] = e;
+          s_int[1] = u0 - before;
+        }
+        before += n;
+      }
+    // rows of items without a visible key are nobody's run: the CTAs share them out
+    for (int e = blockIdx.x; e < a.batch * a.mgroups; e += gridDim.x)
+      if (entry_units(a, e) == 0) {
+        const int b = e / a.mgroups;
+        zero_rows<T, HD>(a, b, e - b * a.mgroups, 0, a.nkv, tid);
+        for (int g = tid; g < a.nkv; g += kThreads) a.cut[e * a.nkv + g] = make_cut(0, 0, 0);
+      }
+    __syncthreads();
+    if (u0 >= u1) return;
+    w.seek(a, s_int[0], s_int[1]);
+  }
 
   const int kw = kWarps / a.nm;            // warps that split an item's keys
   const int mt = warp % a.nm, kg = warp / a.nm;
@@ -786,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * a.irows * HD + 2 * ((size_t)part * a.irows + tid)) =
             make_float2(M, W);
     }
-    if (tid == 0 && w.at == 0)
+    if (tid == 0 && w.at == 0 && !a.whole)
       a.cut[w.e * a.nkv + w.g] = make_cut((u + w.nu - 1) / run - (int)blockIdx.x + 1, blockIdx.x, u != u0 ? 1 : 0);
     asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll 2
@@ -937,9 +958,10 @@ q2_status split_t(const Kv8Attn& a, const uint8_t* kc, const uint8_t* vc, cudaSt
   const uint64_t rows = (uint64_t)a.batch * a.nkv * a.max_seq;
   Q2_TRY(make_tmap_2d_u8(&km, kc, rows, HD, HD, kKeys, HD, HD));
   Q2_TRY(make_tmap_2d_u8(&vm, vc, rows, HD, HD, kKeys, HD, HD));
-  Q2_LAUNCH(kernel, dim3(a.ctas), dim3(kThreads), SM::kTotal, st, true, a, km, vm);
-  // few items: a CTA per row of each, else one per item
   const int items = a.batch * a.nkv * a.mgroups;
+  Q2_LAUNCH(kernel, dim3(a.whole ? items : a.ctas), dim3(kThreads), SM::kTotal, st, true, a, km, vm);
+  if (a.whole) return Q2_OK;
+  // few items: a CTA per row of each, else one per item
   Q2_LAUNCH(kv8_join_kernel<T, HD>, dim3(items, items <= 32 ? a.irows : 1), dim3(kJoinThreads), 0, st, true, a);
   return Q2_OK;
 }
@@ -1060,6 +1082,18 @@ q2_status attn_tc(const Kv8Attn& a, const void* kc, const void* vc, void* ws, si
   return launch_attn_tc(t, ws, a.err, st, r.vnan);
 }
 
+// Whether every item gets a CTA of its own: no scan of the lengths, nothing to
+// join, one launch.  Where a warp has at most six units of an item to itself
+// (12 / 2 heads, us with / without: 64 sequences in caches of 512 positions 8.6 /
+// 13.6, of 1000 12.6 / 14.9, of 2000 21.7 / 20.0), and where items by far outnumber
+// the resident CTAs and are not so long that the last ones leave the machine idle
+// (128 sequences x 8 heads: ragged up to 2000 positions 43 / 55, of 2000 each 62 /
+// 62, of 6000 each 155 / 141).
+bool whole_items(const Kv8Attn& a, const SplitPlan& p) {
+  const long long units = (a.max_seq + kKeys - 1) / kKeys, items = (long long)a.batch * a.nkv * p.mgroups;
+  return units * p.nm <= 24 || (items >= 2 * p.ctas && units <= 128);
+}
+
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
                cudaStream_t st) {
   const SplitPlan p = split_plan(a.batch, a.ntok, a.nh, a.nkv, hd, dtype);
@@ -1075,6 +1109,7 @@ q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, voi
   a.irows = p.irows;
   a.mgroups = p.mgroups;
   a.ctas = p.ctas;
+  a.whole = whole_items(a, p);
   a.cut = static_cast<int4*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.cut_bytes);
   const auto* k = static_cast<const uint8_t*>(kc);
