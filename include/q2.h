@@ -225,8 +225,8 @@ q2_status q2_kv8_read(void* k, void* v, const void* kc, const void* vc, const fl
  * sequence over its 8-bit cache (append first).  lens: device int32 [batch],
  * the positions held, the ntok new ones included; query row t of sequence b
  * sees keys j <= lens[b] - ntok + t.  q [batch, ntok, nh, hd] (the nh * hd
- * elements of a token contiguous; q_strides as k_strides above), out dense;
- * scores, softmax and sums in fp32.  A row that sees no key (a sequence of
+ * elements of a token contiguous; q_strides as k_strides above), out dense and
+ * 16-byte aligned; scores, softmax and sums in fp32.  A row that sees no key (a sequence of
  * length <= 0, or lens[b] < ntok) is zero; lens[b] past max_seq: zero rows and
  * Q2_ERR_CAPACITY in the device error word.  Codes past lens[b] may hold
  * anything.  nh / nkv <= 8.
@@ -240,9 +240,10 @@ q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, c
                            size_t workspace_bytes, void* stream);
 
 /* kv8_self_attention: the same for a block of prompt rows of one sequence:
- * q, out [seqlen, nh, hd] dense, kc, vc [nkv][max_seq][hd], ks, vs [nkv][nblk];
- * query row i sees keys j <= total_len - seqlen + i.  The lengths are the
- * host's. */
+ * q, out [seqlen, nh, hd] dense (out 16-byte aligned), kc, vc [nkv][max_seq]
+ * [hd], ks, vs [nkv][nblk]; query row i sees keys j <= total_len - seqlen + i.
+ * The lengths are the host's.  bf16, hd 128 and 512 rows of a kv head or more
+ * (seqlen * nh / nkv) run on the tcgen05 prompt attention. */
 q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const void* vc,
                                 const float* ks, const float* vs, size_t seqlen, size_t total_len,
                                 size_t nh, size_t nkv, size_t hd, size_t max_seq, float scale,

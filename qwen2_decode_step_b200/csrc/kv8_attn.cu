@@ -289,7 +289,7 @@ __device__ __noinline__ bool prepare_edge(uint8_t* vt, int stale, bool look, int
 
 // Zeroes an m-group's rows of kv heads [g0, g1).
 template <typename T, int HD>
-__device__ __noinline__ void zero_rows(const Kv8Attn& a, int b, int mg, int g0, int g1, int tid) {
+__device__ __forceinline__ void zero_rows(const Kv8Attn& a, int b, int mg, int g0, int g1, int tid) {
   const int r0 = mg * a.irows, n = min(a.irows, a.ntok * a.group - r0) * (HD / 4);
   for (int i = tid; i < (g1 - g0) * n; i += kThreads) {
     const int g = g0 + i / n, r = r0 + i % n / (HD / 4), t = row_tok(a, r);
@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
   using SM = SplitSmem<HD, NT>;
   constexpr bool kWide = sizeof(T) == 4;  // fp32: two fp16 parts of q and of p
   constexpr int kTerms = kWide ? 2 : 1;
+  static_assert(kKeys == 32, "two key tiles a unit");
   constexpr int kMt = kKeys / 16, kC = HD / 16, kW = HD / 16;  // 16-key tiles; 16-dim chunks; words of a lane's key row
   constexpr int kDepth = SM::kDepth, kRows = SM::kRows;
   extern __shared__ __align__(1024) uint8_t kv8_smem_raw[];
@@ -532,15 +533,48 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
           ka[2] = e4m3x2_to_f16x2((uint16_t)(kb[0][j] >> 16));
           ka[3] = e4m3x2_to_f16x2((uint16_t)(kb[1][j] >> 16));
         };
+        if constexpr (kWide) {
+          // fp32: the tensor core cuts each sum's last bit off, so no chain is longer
+          // than two MMAs (and the low terms have one of their own); they are added
+          // with rounding.  One chain of sixteen left 1.3e-6 on outputs where fp32
+          // products leave 0.7e-6.
+          constexpr int kChains = kW < 4 ? kW : 4;
 #pragma unroll
-        for (int h = 0; h < NT; ++h)
+          for (int m = 0; m < kMt; ++m) {
+            float t[kChains + 1][NT][4];
 #pragma unroll
-          for (int m = 0; m < kMt; ++m) s[h][m][0] = s[h][m][1] = s[h][m][2] = s[h][m][3] = 0.f;
-        if constexpr (SM::kQShared) {  // the row tiles are side by side: one key tile at a time
+            for (int x2 = 0; x2 <= kChains; ++x2)
+#pragma unroll
+              for (int h = 0; h < NT; ++h) t[x2][h][0] = t[x2][h][1] = t[x2][h][2] = t[x2][h][3] = 0.f;
+            uint32_t kb[2][kW];
+            load_keys(m, kb);
+#pragma unroll
+            for (int j = 0; j < kW; ++j) {
+              uint32_t ka[4];
+              convert(kb, j, ka);
+#pragma unroll
+              for (int h = 0; h < NT; ++h) {
+                mma_f16(t[j % kChains][h], ka, qb[0][h][j][0], qb[0][h][j][1]);
+                mma_f16(t[kChains][h], ka, qb[kTerms - 1][h][j][0], qb[kTerms - 1][h][j][1]);
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < NT; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float sum = t[0][h][i];
+#pragma unroll
+                for (int x2 = 1; x2 <= kChains; ++x2) sum += t[x2][h][i];
+                s[h][m][i] = sum;
+              }
+          }
+        } else if constexpr (SM::kQShared) {  // the row tiles are side by side: one key tile at a time
 #pragma unroll
           for (int m = 0; m < kMt; ++m) {
             uint32_t kb[2][kW];
             load_keys(m, kb);
+#pragma unroll
+            for (int h = 0; h < NT; ++h) s[h][m][0] = s[h][m][1] = s[h][m][2] = s[h][m][3] = 0.f;
 #pragma unroll
             for (int j = 0; j < kW; ++j) {
               uint32_t ka[4];
@@ -553,16 +587,17 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
             }
           }
         } else {
-          // with one row tile and one term two chains of sums per key tile, added
-          // at the end: a chain of eight MMAs waits for itself
-          constexpr int kChains = NT * kTerms == 1 ? 2 : 1;
-          float s2[kChains == 2 ? kMt : 1][4];
+          // with one row tile two chains of sums per key tile, added at the end: a
+          // chain of eight MMAs waits for itself
+          constexpr int kChains = NT == 1 ? 2 : 1;
+          float s2[kMt][4];
           uint32_t kb[kMt][2][kW];
 #pragma unroll
-          for (int m = 0; m < kMt; ++m) load_keys(m, kb[m]);
-          if constexpr (kChains == 2) {
+          for (int m = 0; m < kMt; ++m) {
+            load_keys(m, kb[m]);
+            s2[m][0] = s2[m][1] = s2[m][2] = s2[m][3] = 0.f;
 #pragma unroll
-            for (int m = 0; m < kMt; ++m) s2[m][0] = s2[m][1] = s2[m][2] = s2[m][3] = 0.f;
+            for (int h = 0; h < NT; ++h) s[h][m][0] = s[h][m][1] = s[h][m][2] = s[h][m][3] = 0.f;
           }
 #pragma unroll
           for (int j = 0; j < kW; ++j)
@@ -572,9 +607,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
               convert(kb[m], j, ka);
 #pragma unroll
               for (int h = 0; h < NT; ++h)
-#pragma unroll
-                for (int e = 0; e < kTerms; ++e)
-                  mma_f16(kChains == 2 && j % 2 ? s2[m] : s[h][m], ka, qb[e][h][j][0], qb[e][h][j][1]);
+                mma_f16(kChains == 2 && j % 2 ? s2[m] : s[h][m], ka, qb[0][h][j][0], qb[0][h][j][1]);
             }
           if constexpr (kChains == 2) {
 #pragma unroll
@@ -619,21 +652,25 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         // ---- softmax: value 2 i + j of tile m is key 16 m + 8 i + gq, row 2 tq + j
         bool grow = false;
         float top[NT][2];
+        auto hidden = [&](int h, int j, int m, int i) { return key0 + 16 * m + 8 * i + gq >= lim[h][j]; };
 #pragma unroll
         for (int h = 0; h < NT; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float f = sc[h][j] * ksc;
-            top[h][j] = -INFINITY;
+            float v[kMt][2];
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                float v = s[h][m][2 * i + j] * f;
-                if (edge && key0 + 16 * m + 8 * i + gq >= lim[h][j]) v = -INFINITY;
-                s[h][m][2 * i + j] = v;
-                top[h][j] = fmaxf(top[h][j], v);
-              }
+              for (int i = 0; i < 2; ++i) v[m][i] = s[h][m][2 * i + j] * f;
+            if (edge) {
+#pragma unroll
+              for (int m = 0; m < kMt; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (hidden(h, j, m, i)) v[m][i] = -INFINITY;
+            }
+            top[h][j] = fmaxf(fmaxf(v[0][0], v[0][1]), fmaxf(v[1][0], v[1][1]));
             grow |= top[h][j] > m_run[h][j] + kGrow;
           }
         if (__any_sync(0xffffffffu, grow)) {
@@ -673,16 +710,20 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         for (int h = 0; h < NT; ++h) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float ms = (m_run[h][j] == -INFINITY ? 0.f : m_run[h][j]) - kPBias;
-            float sum = 0.f;
+            const float f = sc[h][j] * ksc, ms = (m_run[h][j] == -INFINITY ? 0.f : m_run[h][j]) - kPBias;
+            // (one rounding of the difference, small where p is large)
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float p = ex2(s[h][m][2 * i + j] - ms);
-                s[h][m][2 * i + j] = p;
-                sum += p;
-              }
+              for (int i = 0; i < 2; ++i) s[h][m][2 * i + j] = ex2(fmaf(s[h][m][2 * i + j], f, -ms));
+            if (edge) {
+#pragma unroll
+              for (int m = 0; m < kMt; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  if (hidden(h, j, m, i)) s[h][m][2 * i + j] = 0.f;
+            }
+            const float sum = (s[h][0][j] + s[h][0][2 + j]) + (s[h][1][j] + s[h][1][2 + j]);
             l_run[h][j] += sum;
           }
           if (pf != 1.f) {
@@ -716,9 +757,17 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
             const uint32_t va[4] = {e4m3x2_to_f16x2((uint16_t)(y0 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(y0 >> 16)),
                                     e4m3x2_to_f16x2((uint16_t)(y1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(y1 >> 16))};
 #pragma unroll
-            for (int h = 0; h < NT; ++h)
+            for (int h = 0; h < NT; ++h) {
+              if constexpr (kWide) {  // a sum of its own, added with rounding (as the scores)
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(t, va, pb[kTerms - 1][h][kk][0], pb[kTerms - 1][h][kk][1]);
+                mma_f16(t, va, pb[0][h][kk][0], pb[0][h][kk][1]);
 #pragma unroll
-              for (int e = 0; e < kTerms; ++e) mma_f16(o[h][c], va, pb[e][h][kk][0], pb[e][h][kk][1]);
+                for (int j = 0; j < 4; ++j) o[h][c][j] += t[j];
+              } else {
+                mma_f16(o[h][c], va, pb[0][h][kk][0], pb[0][h][kk][1]);
+              }
+            }
           }
         }
         if (edge) fence_async_smem();  // zeroed rows before the slot's next copy
@@ -1007,6 +1056,11 @@ SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd
   return p;
 }
 
+q2_status set_flag(Kv8Attn* a) {
+  a->err = op_error_flag();
+  Q2_CHECK_ARG(a->err, Q2_ERR_CUDA, "cannot resolve the device error flag");
+  return Q2_OK;
+}
 q2_status check_workspace(const void* ws, size_t have, size_t need) {
   if (ws && !(reinterpret_cast<uintptr_t>(ws) & 255) && have >= need) return Q2_OK;
   set_error("kv8 attention: the workspace is NULL, not 256-byte aligned or smaller than "
@@ -1042,9 +1096,10 @@ TcPlan tc_plan(size_t rows, size_t total, size_t nh, size_t nkv) {
   return p;
 }
 
-q2_status attn_tc(const Kv8Attn& a, const void* kc, const void* vc, void* ws, size_t ws_bytes, cudaStream_t st) {
+q2_status attn_tc(Kv8Attn a, const void* kc, const void* vc, void* ws, size_t ws_bytes, cudaStream_t st) {
   const TcPlan p = tc_plan(a.ntok, a.fixed_len, a.nh, a.nkv);
   Q2_TRY(check_workspace(ws, ws_bytes, p.bytes));
+  Q2_TRY(set_flag(&a));
   char* base = static_cast<char*>(ws);
   Q2_CUDA_TRY(cudaMemsetAsync(base, 0, 4096, st));
   Q2_CUDA_TRY(cudaMemsetAsync(base + p.nan, 0, (size_t)a.nkv * 128 * sizeof(int), st));
@@ -1097,11 +1152,12 @@ bool whole_items(const Kv8Attn& a, const SplitPlan& p) {
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
                cudaStream_t st) {
   const SplitPlan p = split_plan(a.batch, a.ntok, a.nh, a.nkv, hd, dtype);
-  Q2_TRY(check_workspace(ws, ws_bytes, p.bytes));
   if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 29)) {
     set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^29");
     return Q2_ERR_SHAPE;
   }
+  Q2_TRY(check_workspace(ws, ws_bytes, p.bytes));
+  Q2_TRY(set_flag(&a));
   a.group = a.nh / a.nkv;
   a.magic = a.group == 1 ? 0u : (unsigned)(((1ull << 32) + a.group - 1) / a.group);
   a.nt = p.nt;
@@ -1133,7 +1189,8 @@ using namespace q2;
 #define Q2_KV8_ATTN_PTRS(who)                                                                                    \
   Q2_CHECK_ARG(out && q && kc && vc && ks && vs, Q2_ERR_INVALID_ARG, who ": NULL pointer");                      \
   Q2_CHECK_ARG(((reinterpret_cast<uintptr_t>(kc) | reinterpret_cast<uintptr_t>(vc)) & 15) == 0,                  \
-               Q2_ERR_INVALID_ARG, who ": the codes must be 16-byte aligned")
+               Q2_ERR_INVALID_ARG, who ": the codes must be 16-byte aligned");                                   \
+  Q2_CHECK_ARG((reinterpret_cast<uintptr_t>(out) & 15) == 0, Q2_ERR_INVALID_ARG, who ": out must be 16-byte aligned")
 
 extern "C" {
 
@@ -1148,8 +1205,6 @@ q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, c
   if (batch == 0 || ntok == 0) return Q2_OK;
   Q2_KV8_ATTN_PTRS("kv8_attention");
   Q2_CHECK_ARG(lens, Q2_ERR_INVALID_ARG, "kv8_attention: NULL lens");
-  int* flag = op_error_flag();
-  Q2_CHECK_ARG(flag, Q2_ERR_CUDA, "cannot resolve the device error flag");
   Q2_CHECK_ARG((unsigned long long)batch * nkv * max_seq < (1ull << 31), Q2_ERR_SHAPE,
                "kv8_attention: need batch * nkv * max_seq < 2^31");
   Kv8Attn a = {};
@@ -1168,7 +1223,6 @@ q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, c
   a.nblk = (int)((max_seq + kBlk - 1) / kBlk);
   a.scale = scale;
   a.out = out;
-  a.err = flag;
   return attn(a, (int)hd, dtype, kc, vc, workspace, workspace_bytes, as_stream(stream));
 }
 
@@ -1183,8 +1237,6 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
   Q2_CHECK_ARG(seqlen < 65536, Q2_ERR_SHAPE, "kv8_self_attention: need seqlen < 65536");
   if (seqlen == 0) return Q2_OK;
   Q2_KV8_ATTN_PTRS("kv8_self_attention");
-  int* flag = op_error_flag();
-  Q2_CHECK_ARG(flag, Q2_ERR_CUDA, "cannot resolve the device error flag");
   Q2_CHECK_ARG((unsigned long long)nkv * max_seq < (1ull << 31), Q2_ERR_SHAPE,
                "kv8_self_attention: need nkv * max_seq < 2^31");
   Kv8Attn a = {};
@@ -1203,7 +1255,6 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
   a.nblk = (int)((max_seq + kBlk - 1) / kBlk);
   a.scale = scale;
   a.out = out;
-  a.err = flag;
   // (the tcgen05 attention reads q and writes out in 16-byte pieces)
   if (use_tc(seqlen, nh / nkv, hd, dtype) &&
       ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0)

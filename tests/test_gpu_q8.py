@@ -233,6 +233,10 @@ ATTN = [  # hd, nh, nkv, max_seq, ntok, lens
     (32, 7, 1, 257, 17, [257, 17, 100]),
     (128, 6, 1, 150, 33, [150, 70]),
     (128, 1, 1, 64, 1, [1]),
+    (128, 12, 2, 900, 1, [899, 0, 64, 33, 32, 700]),
+    (64, 12, 2, 800, 5, [799, 4, 5, 300, 64]),
+    (32, 8, 1, 820, 12, [819, 11, 128]),
+    (128, 8, 1, 800, 40, [800, 500]),
 ]
 
 
@@ -278,6 +282,51 @@ def test_attention_of_a_slot_inside_a_larger_cache():
     q2.q2_kv8_attention(out, qkv.cuda()[:, :, 1:5], *(t[1:] for t in d), i32([99, 4]).cuda(), 0.2)
     ref, bound = R.attention(q, kc[1:], vc[1:], ks[1:], vs[1:], [99, 4], 0.2)
     R.within(out, ref, bound)
+
+
+@pytest.mark.parametrize("dt", DT)
+def test_attention_of_rows_off_16_bytes(dt):
+    """Query tokens an odd number of elements apart, from an odd address."""
+    kc, vc, ks, vs = filled_cache(2, 2, 90, 32, 85)
+    x = randn(86, 2, 3, 4 * 32 + 1).to(DT[dt]).cuda()
+    q = x[..., 1:].unflatten(2, (4, 32))
+    out = torch.empty(2, 3, 4, 32, dtype=DT[dt], device="cuda")
+    q2.q2_kv8_attention(out, q, *both(kc, vc, ks, vs), i32([90, 41]).cuda(), 0.2)
+    ref, bound = R.attention(q.cpu(), kc, vc, ks, vs, [90, 41], 0.2)
+    R.within(out, ref, bound)
+
+
+def test_prompt_rows_off_16_bytes():
+    """The prompt path that reads q in 16-byte pieces gives way to the other one."""
+    kc, vc, ks, vs = filled_cache(1, 1, 300, 128, 87)
+    x = randn(88, 260 * 2 * 128 + 1).bfloat16().cuda()[1:].view(260, 2, 128)
+    d = both(kc, vc, ks, vs)
+    out = torch.empty_like(x.clone())
+    q2.q2_kv8_self_attention(out, x, *(t[0] for t in d), 300, 0.09)
+    ref, bound = R.attention(x.cpu()[None], kc, vc, ks, vs, [300], 0.09)
+    R.within(out, ref[0], bound[0])
+
+
+def test_many_short_and_few_long_items_take_the_same_values():
+    """One CTA per item (a short cache, or items in plenty) and runs over all items: the same
+    sequences in a cache with room for 256 positions and for 4096, and 512 of them."""
+    B, nkv, hd, nh, S = 3, 2, 64, 6, 256
+    kc, vc, ks, vs = filled_cache(B, nkv, S, hd, 89)
+    lens = [256, 77, 0]
+    q = randn(89, B, 1, nh, hd).bfloat16()
+    ref, bound = R.attention(q, kc, vc, ks, vs, lens, 0.125)
+    small = torch.empty(B, 1, nh, hd, dtype=torch.bfloat16, device="cuda")
+    q2.q2_kv8_attention(small, q.cuda(), *both(kc, vc, ks, vs), i32(lens).cuda(), 0.125)
+    R.within(small, ref, bound, "short cache")
+    wide = [torch.cat([t, torch.full((*t.shape[:2], (4096 - S) // (1 if t.dim() == 4 else 64), *t.shape[3:]), 127,
+                                     dtype=t.dtype)], 2) for t in (kc, vc, ks, vs)]
+    large = torch.empty_like(small)
+    q2.q2_kv8_attention(large, q.cuda(), *both(*wide), i32(lens).cuda(), 0.125)
+    R.within(large, ref, bound, "long cache")
+    many = [t.repeat(171, *[1] * (t.dim() - 1)).contiguous().cuda() for t in (kc, vc, ks, vs)]
+    out = torch.empty(B * 171, 1, nh, hd, dtype=torch.bfloat16, device="cuda")
+    q2.q2_kv8_attention(out, q.repeat(171, 1, 1, 1).cuda(), *many, i32(lens * 171).cuda(), 0.125)
+    assert torch.equal(out.view(171, B, 1, nh, hd), small.expand(171, B, 1, nh, hd))
 
 
 @pytest.mark.parametrize("dt", DT)

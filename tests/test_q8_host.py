@@ -87,6 +87,8 @@ def test_attention_calls_refuse(call):
     for p in ("out", "q", "kc", "vc", "ks", "vs"):
         assert call(**{p: None}) == 1
     assert call(kc=264) == 1 and call(vc=260) == 1
+    assert call(out=264) == 1
+    assert call(ws=None) == 1 and call(ws=300) == 1 and call(ws_bytes=100) == 1
 
 
 def test_attention_length_refusals():
@@ -101,6 +103,15 @@ def test_attention_workspace_refusals():
     assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 13, 2, 128, 1, ctypes.byref(n)) == 3
     assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 7, ctypes.byref(n)) == 2
     assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 1, None) == 1
+    assert _raw("q2_kv8_attention_workspace", 2, 4, 64, 12, 2, 128, 1, ctypes.byref(n)) == 3  # a total_len is one sequence's
+    assert _raw("q2_kv8_attention_workspace", 1, 65, 64, 12, 2, 128, 1, ctypes.byref(n)) == 3
+    assert _raw("q2_kv8_attention_workspace", 0, 1, 0, 12, 2, 128, 1, ctypes.byref(n)) == 0 and n.value == 0
+
+
+def test_attention_sizes_past_its_counters_are_refused():
+    assert _attn(batch=32767, nkv=2, max_seq=1 << 20) == 3      # batch * nkv * max_seq
+    assert _attn(batch=16, ntok=65535, max_seq=1 << 20) == 3    # times the row groups and blocks
+    assert _self(seqlen=65536, total=65536, max_seq=1 << 20) == 3
 
 
 def test_quantize_refuses():
