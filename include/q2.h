@@ -231,8 +231,8 @@ q2_status q2_kv8_read(void* k, void* v, const void* kc, const void* vc, const fl
  * Q2_ERR_CAPACITY in the device error word.  Codes past lens[b] may hold
  * anything.  nh / nkv <= 8.
  * workspace: device memory of at least q2_kv8_attention_workspace() bytes,
- * 256-byte aligned, contents ignored; calls that may overlap on the GPU need
- * one each. */
+ * 256-byte aligned, contents ignored (NULL where that is 0); calls that may
+ * overlap on the GPU need one each. */
 q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, const void* kc,
                            const void* vc, const float* ks, const float* vs, const int32_t* lens,
                            size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd,
@@ -251,9 +251,10 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
 
 /* The workspace that kv8_attention (total_len = 0) or kv8_self_attention
  * (batch = 1, ntok = seqlen, total_len) needs on the current device, in
- * *bytes. */
+ * *bytes; 0 for a batch over short caches. */
 q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len, size_t nh,
-                                     size_t nkv, size_t hd, int dtype, size_t* bytes);
+                                     size_t nkv, size_t hd, size_t max_seq, int dtype,
+                                     size_t* bytes);
 
 /* ---- 8-bit linear --------------------------------------------------------
  * Operands in e4m3 with an fp32 scale per group of Q2_Q8_GROUP elements along

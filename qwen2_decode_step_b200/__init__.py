@@ -74,7 +74,7 @@ _SIGS = {
     "q2_kv8_attention": [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _F, _I, _VP, _SZ,
                          _VP],
     "q2_kv8_self_attention": [_VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _F, _I, _VP, _SZ, _VP],
-    "q2_kv8_attention_workspace": [_SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _I, ctypes.POINTER(_SZ)],
+    "q2_kv8_attention_workspace": [_SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _SZ, _I, ctypes.POINTER(_SZ)],
     "q2_quantize_q8": [_VP, _VP, _VP, _SZ, _SZ, _SZ, _I, _I, _VP],
     "q2_linear_q8": [_VP, _VP, _VP, _VP, _VP, _VP, _SZ, _SZ, _SZ, _I, _VP],
     "q2_model_create": [ctypes.POINTER(_Meta), _I, ctypes.POINTER(_VP)],
@@ -351,7 +351,16 @@ def _tok_strides(t):
     s = t.stride()
     if (d > 1 and s[3] != 1) or (h > 1 and s[2] != d):
         raise ValueError("the heads of a token must be contiguous")
-    return (ctypes.c_int64 * 2)(s[0], s[1])
+    key = (s[0], s[1])
+    pair = _stride_pairs.get(key)  # (building one takes as long as a launch's half)
+    if pair is None:
+        if len(_stride_pairs) >= 4096:
+            _stride_pairs.clear()
+        pair = _stride_pairs[key] = (ctypes.c_int64 * 2)(*key)
+    return pair
+
+
+_stride_pairs: Dict[Tuple[int, int], ctypes.Array] = {}
 
 
 def q2_kv8_append(kc, vc, ks, vs, k, v, start):
@@ -390,14 +399,14 @@ def q2_kv8_read(k, v, kc, vc, ks, vs, start):
 _ws_bytes: Dict[Tuple, int] = {}
 
 
-def q2_kv8_attention_workspace(batch, ntok, nh, nkv, hd, dtype=torch.bfloat16, total_len=0) -> int:
+def q2_kv8_attention_workspace(batch, ntok, nh, nkv, hd, max_seq, dtype=torch.bfloat16, total_len=0) -> int:
     """Bytes of workspace that q2_kv8_attention (total_len = 0) or q2_kv8_self_attention
-    (batch = 1, ntok = its rows) needs on the current device."""
-    key = (torch._C._cuda_getDevice(), batch, ntok, nh, nkv, hd, dtype, total_len)
+    (batch = 1, ntok = its rows) needs on the current device for a cache of max_seq positions."""
+    key = (torch._C._cuda_getDevice(), batch, ntok, nh, nkv, hd, max_seq, dtype, total_len)
     n = _ws_bytes.get(key)
     if n is None:
         c = _SZ(0)
-        _call("q2_kv8_attention_workspace", batch, ntok, total_len, nh, nkv, hd, _DT[dtype], ctypes.byref(c))
+        _call("q2_kv8_attention_workspace", batch, ntok, total_len, nh, nkv, hd, max_seq, _DT[dtype], ctypes.byref(c))
         if len(_ws_bytes) >= 4096:
             _ws_bytes.clear()
         n = _ws_bytes[key] = c.value
@@ -405,13 +414,19 @@ def q2_kv8_attention_workspace(batch, ntok, nh, nkv, hd, dtype=torch.bfloat16, t
 
 
 def _workspace(ws, like, *args):
-    """The caller's workspace, or one from torch's allocator (stream-ordered, a graph's own)."""
+    """The caller's workspace, or one from torch's allocator (stream-ordered, a graph's own);
+    None where the call needs none."""
     if ws is None:
-        return torch.empty(q2_kv8_attention_workspace(*args), dtype=torch.uint8, device=like.device)
+        n = q2_kv8_attention_workspace(*args)
+        return torch.empty(n, dtype=torch.uint8, device=like.device) if n else None
     if ws.dtype is not torch.uint8 or not ws.is_contiguous():
         _refuse("workspace", (ws, ws.shape, _U8_ONLY))
     _here(like, ws)
     return ws
+
+
+def _ptr_size(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
 def q2_kv8_attention(out, q, kc, vc, ks, vs, lens, scale, workspace=None):
@@ -427,10 +442,10 @@ def q2_kv8_attention(out, q, kc, vc, ks, vs, lens, scale, workspace=None):
             and lens.dtype is torch.int32 and lens.is_contiguous()):
         _refuse("kv8_attention", (out, q.shape, (q.dtype,)), (lens, (B,), _I32_ONLY))
     stream = _here(out, q, kc, vc, ks, vs, lens)
-    ws = _workspace(workspace, q, B, T, nh, nkv, hd, q.dtype)
+    ws = _workspace(workspace, q, B, T, nh, nkv, hd, S, q.dtype)
     _call("q2_kv8_attention", out.data_ptr(), q.data_ptr(), _tok_strides(q), kc.data_ptr(), vc.data_ptr(),
-          ks.data_ptr(), vs.data_ptr(), lens.data_ptr(), B, T, nh, nkv, hd, S, scale, _dtype(q), ws.data_ptr(),
-          ws.numel(), stream)
+          ks.data_ptr(), vs.data_ptr(), lens.data_ptr(), B, T, nh, nkv, hd, S, scale, _dtype(q), *_ptr_size(ws),
+          stream)
     return out
 
 
@@ -444,9 +459,9 @@ def q2_kv8_self_attention(out, q, kc, vc, ks, vs, total_len, scale, workspace=No
             and out.is_contiguous()):
         _refuse("kv8_self_attention", (q, (T, nh, hd), _BF16_OR_F32), (out, (T, nh, hd), (q.dtype,)))
     stream = _here(out, q, kc, vc, ks, vs)
-    ws = _workspace(workspace, q, 1, T, nh, nkv, hd, q.dtype, total_len)
+    ws = _workspace(workspace, q, 1, T, nh, nkv, hd, S, q.dtype, total_len)
     _call("q2_kv8_self_attention", out.data_ptr(), q.data_ptr(), kc.data_ptr(), vc.data_ptr(), ks.data_ptr(),
-          vs.data_ptr(), T, total_len, nh, nkv, hd, S, scale, _dtype(q), ws.data_ptr(), ws.numel(), stream)
+          vs.data_ptr(), T, total_len, nh, nkv, hd, S, scale, _dtype(q), *_ptr_size(ws), stream)
     return out
 
 

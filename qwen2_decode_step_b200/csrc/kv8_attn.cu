@@ -80,7 +80,7 @@ struct Kv8Attn {
   float* part;  // [2 * CTAs][irows][hd + 2]: rows of partial items, then m and l of each row
   int4* cut;    // [items]: how the runs cut each item
   int ctas;     // of the split kernel
-  int whole;    // a CTA per item, nothing is cut (see whole_items)
+  int whole;    // a CTA per item, nothing is cut (see split_plan)
   int* err;
 };
 
@@ -1035,9 +1035,10 @@ q2_status split(const Kv8Attn& a, int hd, const uint8_t* kc, const uint8_t* vc, 
 // the split kernel.
 struct SplitPlan {
   int nt, nm, irows, mgroups, ctas;
+  bool whole;  // every item gets a CTA of its own
   size_t cut_bytes, bytes;
 };
-SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd, int dtype) {
+SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd, size_t max_seq, int dtype) {
   SplitPlan p;
   const int rows = (int)(ntok * (nh / nkv));
   // Four tiles convert K and V half as often as two, but leave a warp alone with
@@ -1051,8 +1052,17 @@ SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd
   p.mgroups = ceil_div(rows, p.irows);
   p.ctas = num_sms() * (p.nt == 1 ? 3 : 2);  // all resident at once
   if (p.ctas > kCtasMax) p.ctas = kCtasMax;
-  p.cut_bytes = (batch * p.mgroups * nkv * sizeof(int4) + 255) / 256 * 256;
-  p.bytes = p.cut_bytes + (size_t)2 * p.ctas * p.irows * (hd + 2) * sizeof(float);
+  // Items whole: no scan of the lengths, nothing to join, one launch, no
+  // workspace.  Where a warp has at most six units of an item to itself (12 / 2
+  // heads, us with / without: 64 sequences in caches of 512 positions 8.6 / 13.6,
+  // of 1000 12.6 / 14.9, of 2000 21.7 / 20.0), and where items by far outnumber the
+  // resident CTAs and are not so long that the last ones leave the machine idle
+  // (128 sequences x 8 heads: ragged up to 2000 positions 43 / 55, of 2000 each 62
+  // / 62, of 6000 each 155 / 141).
+  const unsigned long long units = (max_seq + kKeys - 1) / kKeys, items = (unsigned long long)batch * nkv * p.mgroups;
+  p.whole = units * p.nm <= 24 || (items >= 2ull * p.ctas && units <= 128);
+  p.cut_bytes = (items * sizeof(int4) + 255) / 256 * 256;
+  p.bytes = p.whole ? 0 : p.cut_bytes + (size_t)2 * p.ctas * p.irows * (hd + 2) * sizeof(float);
   return p;
 }
 
@@ -1062,7 +1072,7 @@ q2_status set_flag(Kv8Attn* a) {
   return Q2_OK;
 }
 q2_status check_workspace(const void* ws, size_t have, size_t need) {
-  if (ws && !(reinterpret_cast<uintptr_t>(ws) & 255) && have >= need) return Q2_OK;
+  if (need == 0 || (ws && !(reinterpret_cast<uintptr_t>(ws) & 255) && have >= need)) return Q2_OK;
   set_error("kv8 attention: the workspace is NULL, not 256-byte aligned or smaller than "
             "q2_kv8_attention_workspace says");
   return Q2_ERR_INVALID_ARG;
@@ -1137,21 +1147,9 @@ q2_status attn_tc(Kv8Attn a, const void* kc, const void* vc, void* ws, size_t ws
   return launch_attn_tc(t, ws, a.err, st, r.vnan);
 }
 
-// Whether every item gets a CTA of its own: no scan of the lengths, nothing to
-// join, one launch.  Where a warp has at most six units of an item to itself
-// (12 / 2 heads, us with / without: 64 sequences in caches of 512 positions 8.6 /
-// 13.6, of 1000 12.6 / 14.9, of 2000 21.7 / 20.0), and where items by far outnumber
-// the resident CTAs and are not so long that the last ones leave the machine idle
-// (128 sequences x 8 heads: ragged up to 2000 positions 43 / 55, of 2000 each 62 /
-// 62, of 6000 each 155 / 141).
-bool whole_items(const Kv8Attn& a, const SplitPlan& p) {
-  const long long units = (a.max_seq + kKeys - 1) / kKeys, items = (long long)a.batch * a.nkv * p.mgroups;
-  return units * p.nm <= 24 || (items >= 2 * p.ctas && units <= 128);
-}
-
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,
                cudaStream_t st) {
-  const SplitPlan p = split_plan(a.batch, a.ntok, a.nh, a.nkv, hd, dtype);
+  const SplitPlan p = split_plan(a.batch, a.ntok, a.nh, a.nkv, hd, a.max_seq, dtype);
   if ((unsigned long long)a.batch * a.nkv * p.mgroups * a.nblk >= (1ull << 29)) {
     set_error("kv8 attention: batch * kv heads * query row groups * key blocks must stay below 2^29");
     return Q2_ERR_SHAPE;
@@ -1165,7 +1163,7 @@ q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, voi
   a.irows = p.irows;
   a.mgroups = p.mgroups;
   a.ctas = p.ctas;
-  a.whole = whole_items(a, p);
+  a.whole = p.whole;
   a.cut = static_cast<int4*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.cut_bytes);
   const auto* k = static_cast<const uint8_t*>(kc);
@@ -1263,17 +1261,16 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
 }
 
 q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len, size_t nh, size_t nkv, size_t hd,
-                                     int dtype, size_t* bytes) {
+                                     size_t max_seq, int dtype, size_t* bytes) {
   clear_error();
-  const size_t max_seq = 1;
   Q2_KV8_ATTN_CHECK("kv8_attention_workspace");
   Q2_CHECK_ARG(bytes, Q2_ERR_INVALID_ARG, "kv8_attention_workspace: NULL bytes");
   Q2_CHECK_ARG(ntok < 65536, Q2_ERR_SHAPE, "kv8_attention_workspace: need ntok < 65536");
-  Q2_CHECK_ARG(total_len == 0 || (batch == 1 && ntok <= total_len && total_len < (1u << 30)), Q2_ERR_SHAPE,
-               "kv8_attention_workspace: with a total_len, batch must be 1 and ntok at most total_len");
+  Q2_CHECK_ARG(total_len == 0 || (batch == 1 && ntok <= total_len && total_len <= max_seq), Q2_ERR_SHAPE,
+               "kv8_attention_workspace: with a total_len, batch must be 1, ntok at most total_len and that at most max_seq");
   *bytes = 0;
   if (batch == 0 || ntok == 0) return Q2_OK;
-  *bytes = split_plan(batch, ntok, nh, nkv, hd, dtype).bytes;
+  *bytes = split_plan(batch, ntok, nh, nkv, hd, max_seq, dtype).bytes;
   if (total_len && use_tc(ntok, nh / nkv, hd, dtype)) {
     const size_t tc = tc_plan(ntok, total_len, nh, nkv).bytes;
     if (tc > *bytes) *bytes = tc;  // (either path, as the alignment of q and out has it)

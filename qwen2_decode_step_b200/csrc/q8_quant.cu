@@ -36,20 +36,55 @@ struct Share {
   static constexpr int kV = VEC ? Storage<T>::kVec : 4;   // elements of a lane
   static constexpr int kLanes = kGroup / kV;              // lanes of a row: 32, or 16 (bf16 vectors)
   static constexpr int kRows = 32 / kLanes;               // rows of a warp's step
-  static __device__ __forceinline__ void load(const T* row, int c0, int cols, float* f) {
+  uint4 raw;                                              // as stored (VEC), or four fp32 values
+  __device__ __forceinline__ void load(const T* row, int c0, int cols) {
     const int l = threadIdx.x % kLanes;
     if constexpr (VEC) {
       const int c = c0 + l * kV;
-      if (c < cols) {
-        unpack16<T>(*reinterpret_cast<const uint4*>(row + c), f);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) f[j] = 0.f;
-      }
+      raw = c < cols ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u);
     } else {
+      uint32_t* w = &raw.x;
 #pragma unroll
-      for (int j = 0; j < kV; ++j) f[j] = c0 + l + 32 * j < cols ? to_f(row[c0 + l + 32 * j]) : 0.f;
+      for (int j = 0; j < kV; ++j) w[j] = __float_as_uint(c0 + l + 32 * j < cols ? to_f(row[c0 + l + 32 * j]) : 0.f);
     }
+  }
+  __device__ __forceinline__ void values(float* f) const {
+    if constexpr (VEC)
+      unpack16<T>(raw, f);
+    else
+      unpack16<float>(raw, f);
+  }
+  // The largest finite magnitude (the maxima pass over NaN); `inf` says whether an
+  // infinity was among them, which is rare and settled out of the way of the
+  // others.  bf16 pairs are compared as they are: half the instructions.
+  __device__ __forceinline__ float amax(bool* inf) const {
+    float m;
+    if constexpr (VEC && sizeof(T) == 2) {
+      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+      __nv_bfloat162 a[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = w[i] & 0x7fff7fffu;
+        a[i] = *reinterpret_cast<const __nv_bfloat162*>(&v);
+      }
+      const __nv_bfloat162 x = __hmax2(__hmax2(a[0], a[1]), __hmax2(a[2], a[3]));
+      m = fmaxf(__low2float(x), __high2float(x));
+    } else {
+      float f[kV];
+      values(f);
+      m = fabsf(f[0]);
+#pragma unroll
+      for (int j = 1; j < kV; ++j) m = fmaxf(m, fabsf(f[j]));
+    }
+    *inf = m == INFINITY;
+    if (*inf) {
+      float f[kV];
+      values(f);
+      m = 0.f;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) m = fmaxf(m, finite_abs(f[j]));
+    }
+    return m;
   }
   static __device__ __forceinline__ void store(uint8_t* row, int c0, int cols, const float* f) {
     const int l = threadIdx.x % kLanes;
@@ -70,23 +105,6 @@ struct Share {
     }
   }
 };
-
-// The largest finite magnitude of a lane's N elements (fmaxf passes over NaN);
-// `inf` says whether an infinity was among them, which is rare and settled out
-// of the way of the others.
-template <int N>
-__device__ __forceinline__ float lane_amax(const float* f, bool* inf) {
-  float m = fabsf(f[0]);
-#pragma unroll
-  for (int j = 1; j < N; ++j) m = fmaxf(m, fabsf(f[j]));
-  *inf = m == INFINITY;
-  if (*inf) {
-    m = 0.f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) m = fmaxf(m, finite_abs(f[j]));
-  }
-  return m;
-}
 
 // x * (448 / a) of N elements, in place (infinities go to +-448 here: times lo
 // they would become NaN).
@@ -119,21 +137,23 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const Quant a) {
   const int rc = blockIdx.x / chunks, g0 = (blockIdx.x - rc * chunks) * kRowGroups;
   const int row = (rc * 8 + warp) * S::kRows + lane / S::kLanes;
   const int cols = row < a.rows ? a.cols : 0;
-  float f[kRowGroups][S::kV];
+  S in[kRowGroups];
 #pragma unroll
   for (int i = 0; i < kRowGroups; ++i)
-    S::load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, (g0 + i) * kGroup, cols, f[i]);
+    in[i].load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, (g0 + i) * kGroup, cols);
 #pragma unroll
   for (int i = 0; i < kRowGroups; ++i) {
     bool inf;
-    float m = lane_amax<S::kV>(f[i], &inf);
+    float m = in[i].amax(&inf);
 #pragma unroll
     for (int o = 1; o < S::kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     m = fmaxf(m, 0x1p-100f);
     float hi, lo;
     quotient(m, &hi, &lo);
-    to_code_range<S::kV>(f[i], m, hi, lo, inf);
-    S::store(a.codes + (size_t)row * a.cols, (g0 + i) * kGroup, cols, f[i]);
+    float f[S::kV];
+    in[i].values(f);
+    to_code_range<S::kV>(f, m, hi, lo, inf);
+    S::store(a.codes + (size_t)row * a.cols, (g0 + i) * kGroup, cols, f);
     if (lane % S::kLanes == 0 && row < a.rows && g0 + i < a.groups)
       a.scales[(size_t)(g0 + i) * a.rows + row] = __fdiv_rn(m, kE4m3Max);
   }
@@ -151,18 +171,18 @@ __global__ void __launch_bounds__(512) quant_blocks_kernel(const Quant a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = blockIdx.x, rb = blockIdx.y;
   const int row0 = rb * 128 + warp * S::kRows + lane / S::kLanes;
-  float f[kSteps][S::kV];
+  S in[kSteps];
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int row = row0 + 16 * S::kRows * i;
-    S::load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, g * kGroup, row < a.rows ? a.cols : 0, f[i]);
+    in[i].load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, g * kGroup, row < a.rows ? a.cols : 0);
   }
   bool any_inf = false;
   float m = 0.f;
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     bool inf;
-    m = fmaxf(m, lane_amax<S::kV>(f[i], &inf));
+    m = fmaxf(m, in[i].amax(&inf));
     any_inf |= inf;
   }
   m = warp_max(m);
@@ -176,8 +196,10 @@ __global__ void __launch_bounds__(512) quant_blocks_kernel(const Quant a) {
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int row = row0 + 16 * S::kRows * i;
-    to_code_range<S::kV>(f[i], m, hi, lo, any_inf);
-    S::store(a.codes + (size_t)row * a.cols, g * kGroup, row < a.rows ? a.cols : 0, f[i]);
+    float f[S::kV];
+    in[i].values(f);
+    to_code_range<S::kV>(f, m, hi, lo, any_inf);
+    S::store(a.codes + (size_t)row * a.cols, g * kGroup, row < a.rows ? a.cols : 0, f);
   }
   if (threadIdx.x == 0) a.scales[(size_t)rb * a.groups + g] = __fdiv_rn(m, kE4m3Max);
 }

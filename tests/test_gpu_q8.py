@@ -569,7 +569,7 @@ def test_two_calls_at_once_have_a_workspace_each():
 
 
 def test_workspace_too_small_is_refused():
-    kc, vc, ks, vs = both(*filled_cache(1, 2, 300, 128, 152))
+    kc, vc, ks, vs = both(*empty_cache(1, 2, 3000, 128))
     q = randn(153, 1, 1, 4, 128).cuda()
     with pytest.raises(q2.Q2Error) as e:
         q2.q2_kv8_attention(torch.empty_like(q), q, kc, vc, ks, vs, i32([300]).cuda(), 1.0,

@@ -88,7 +88,8 @@ def test_attention_calls_refuse(call):
         assert call(**{p: None}) == 1
     assert call(kc=264) == 1 and call(vc=260) == 1
     assert call(out=264) == 1
-    assert call(ws=None) == 1 and call(ws=300) == 1 and call(ws_bytes=100) == 1
+    for bad in ({"ws": None}, {"ws": 300}, {"ws_bytes": 100}):
+        assert call(max_seq=8192, **bad) == 1
 
 
 def test_attention_length_refusals():
@@ -100,12 +101,14 @@ def test_attention_length_refusals():
 
 def test_attention_workspace_refusals():
     n = ctypes.c_size_t(0)
-    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 13, 2, 128, 1, ctypes.byref(n)) == 3
-    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 7, ctypes.byref(n)) == 2
-    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 1, None) == 1
-    assert _raw("q2_kv8_attention_workspace", 2, 4, 64, 12, 2, 128, 1, ctypes.byref(n)) == 3  # a total_len is one sequence's
-    assert _raw("q2_kv8_attention_workspace", 1, 65, 64, 12, 2, 128, 1, ctypes.byref(n)) == 3
-    assert _raw("q2_kv8_attention_workspace", 0, 1, 0, 12, 2, 128, 1, ctypes.byref(n)) == 0 and n.value == 0
+    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 13, 2, 128, 64, 1, ctypes.byref(n)) == 3
+    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 64, 7, ctypes.byref(n)) == 2
+    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 64, 1, None) == 1
+    assert _raw("q2_kv8_attention_workspace", 2, 4, 64, 12, 2, 128, 64, 1, ctypes.byref(n)) == 3  # a total_len is one sequence's
+    assert _raw("q2_kv8_attention_workspace", 1, 65, 64, 12, 2, 128, 64, 1, ctypes.byref(n)) == 3
+    assert _raw("q2_kv8_attention_workspace", 0, 1, 0, 12, 2, 128, 64, 1, ctypes.byref(n)) == 0 and n.value == 0
+    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 64, 1, ctypes.byref(n)) == 0 and n.value == 0
+    assert _raw("q2_kv8_attention_workspace", 1, 1, 0, 12, 2, 128, 4096, 1, ctypes.byref(n)) == 0 and n.value > 0
 
 
 def test_attention_sizes_past_its_counters_are_refused():
