@@ -6,6 +6,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "kernels.h"
 #include "gemm_tc.h"
 

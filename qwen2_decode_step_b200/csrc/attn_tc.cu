@@ -52,6 +52,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv8.h"
 #include "tma.h"
 
 namespace q2 {
@@ -630,7 +631,11 @@ bool attn_tc_supported(const AttnRows& a, int dtype) {
          (reinterpret_cast<uintptr_t>(seq_v(a)) & 15) == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0;
 }
 
-q2_status launch_attn_tc(const AttnRows& a, void* ws, int* err, cudaStream_t st, const int* vnan) {
+q2_status launch_attn_tc(const AttnRows& a, void* ws, int* err, cudaStream_t st) {
+  return launch_attn_tc_nan(a, ws, err, st, nullptr);
+}
+
+q2_status launch_attn_tc_nan(const AttnRows& a, void* ws, int* err, cudaStream_t st, const int* vnan) {
   if (a.rows == 0) return Q2_OK;
   const int pos0 = a.base - 1;
   const long long keys = (long long)pos0 + a.rows;  // keys visible to the last row

@@ -8,7 +8,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
 #include <string>
 #include <utility>
 
@@ -52,16 +51,14 @@ inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s
 // that loads the library.  Every error word (this one and each model's) uses
 // the same bits: value 1 = a token id outside [0, vocab); value 2 = a
 // bounded device-side wait ran out (a pipeline or grid-phase dependency that
-// never arrived); value 4 = a device-side length past the capacity of an 8-bit
-// cache.
+// never arrived).
 int* op_error_flag();
 constexpr int kErrIndex = 1;
 constexpr int kErrTimeout = 2;
-constexpr int kErrCapacity = 4;
 
 // The status (and message) of a nonzero error word: Q2_ERR_TIMEOUT if a wait
 // ran out (it takes precedence: the results are undefined), else
-// Q2_ERR_INDEX, else Q2_ERR_CAPACITY.  `who` prefixes the message.
+// Q2_ERR_INDEX.  `who` prefixes the message.
 q2_status device_error_status(int bits, const char* who);
 
 // ------------------------------------------------------------ storage types
@@ -274,21 +271,6 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-}  // namespace q2
-
-namespace q2 {
-// Whether this is the first call on the current device for `done` (one bit per
-// device; a kernel's attributes are set once).  Devices past 63 always set them.
-inline bool first_on_device(std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev > 63) return true;
-  return (done.load(std::memory_order_acquire) >> dev & 1) == 0;
-}
-inline void done_on_device(std::atomic<uint64_t>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev <= 63)
-    done.fetch_or(1ull << dev, std::memory_order_release);
 }
 }  // namespace q2
 

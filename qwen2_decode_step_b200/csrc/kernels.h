@@ -90,10 +90,6 @@ size_t attn_tc_ws_bytes();
 void attn_tc_plan(int rows, int pos0, int nh, int sms, bool split_ok, int* n_whole, int* ts);
 int attn_tc_slot_capacity(int sms);
 int attn_tc_counter_capacity();
-// What one call of this size needs of the scratch (counters, then its slots).
-size_t attn_tc_ws_need(int rows, int pos0, int nh);
-// vnan: null, or int [nkv][hd]: INT32_MAX - p for a V with its first NaN of that
-// dim at position p (taken out of V), 0 for none; rows from p on get NaN there.
-q2_status launch_attn_tc(const AttnRows& a, void* ws, int* err, cudaStream_t st, const int* vnan = nullptr);
+q2_status launch_attn_tc(const AttnRows& a, void* ws, int* err, cudaStream_t st);
 
 }  // namespace q2

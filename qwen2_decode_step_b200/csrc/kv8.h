@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/q2.h"
+#include "kernels.h"
 
 namespace q2 {
 
@@ -24,5 +25,12 @@ struct Kv8Read {
   int* vnan;
 };
 q2_status launch_kv8_read(const Kv8Read& a, int dtype, int* err, cudaStream_t st);
+
+// launch_attn_tc with V's NaN kept apart: vnan is null, or int [nkv][hd] with
+// INT32_MAX - p for a V with its first NaN of that dim at position p (taken out
+// of V), 0 for none; rows from p on get NaN there.
+q2_status launch_attn_tc_nan(const AttnRows& a, void* ws, int* err, cudaStream_t st, const int* vnan);
+// What one call of this size needs of its scratch (counters, then its slots).
+size_t attn_tc_ws_need(int rows, int pos0, int nh);
 
 }  // namespace q2

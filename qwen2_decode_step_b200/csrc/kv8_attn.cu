@@ -1144,7 +1144,7 @@ q2_status attn_tc(Kv8Attn a, const void* kc, const void* vc, void* ws, size_t ws
   t.base = a.fixed_len - a.ntok + 1;
   t.row_step = 1;
   t.scale = a.scale;
-  return launch_attn_tc(t, ws, a.err, st, r.vnan);
+  return launch_attn_tc_nan(t, ws, a.err, st, r.vnan);
 }
 
 q2_status attn(Kv8Attn a, int hd, int dtype, const void* kc, const void* vc, void* ws, size_t ws_bytes,

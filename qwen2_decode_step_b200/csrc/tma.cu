@@ -2,6 +2,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "tma.h"
 
 namespace q2 {

@@ -17,19 +17,9 @@ q2_status make_tmap_2d_bf16(CUtensorMap* out, const void* base, uint64_t rows, u
                             uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols,
                             int swizzle_bytes);
 
-// The same for bytes (e4m3 codes): box_cols bytes wide.
-q2_status make_tmap_2d_u8(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
-                          uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols,
-                          int swizzle_bytes);
-
-// The same for fp32.
-q2_status make_tmap_2d_f32(CUtensorMap* out, const void* base, uint64_t rows, uint64_t cols,
-                           uint64_t pitch_bytes, uint32_t box_rows, uint32_t box_cols,
-                           int swizzle_bytes);
-
 // Tiled 2-D TMA load of one box at (x = column, y = row) into shared memory,
 // completing on `bar` (transaction bytes).  The column coordinate must be a
-// multiple of 8 for bf16, of 16 for bytes (16-byte alignment of the innermost coordinate);
+// multiple of 8 for bf16 (16-byte alignment of the innermost coordinate);
 // rows beyond the tensor read as zeros.  No multicast.
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, int x, int y,
                                             uint64_t* bar) {
@@ -40,21 +30,5 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       "r"(static_cast<uint32_t>(__cvta_generic_to_shared(bar)))
       : "memory");
 }
-
-// Tiled 2-D TMA store of one box of shared memory to (x = column, y = row), in
-// the issuing thread's current bulk group; elements outside the tensor are not
-// written.  x and y must not be negative, x as for tma_load_2d.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* smem_src) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(static_cast<uint32_t>(__cvta_generic_to_shared(smem_src)))
-               : "memory");
-}
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// Every bulk group of this thread has read its shared memory / is complete.
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// Generic writes to shared memory before this are seen by later async-proxy reads.
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 }  // namespace q2
