@@ -3,14 +3,16 @@
 //
 //   a = max(largest finite |x| of the group, 2^-100)
 //   scale = a / 448,  code = e4m3(x * (448 / a))
-// Two divisions per group and none per element (an IEEE division each would
-// cost more issue slots than the loads leave): 448 / a is kept as hi + lo, lo
-// the remainder of the rounded quotient, and x * hi + x * lo is one fused
-// rounding from the quotient of the definition, where x * hi alone would fall
-// on the other side of a code's border about three times as often.  The lower
-// bound on a keeps 448 / a finite; a group of zeros gets codes of 0.
+// 448 / a is kept as hi + lo to some 45 bits, hi an approximate quotient and lo
+// its remainder over a, and x * hi + x * lo is one rounding from the definition's
+// product, where x times a rounded quotient alone would fall on the other side of
+// a code's border about three times as often.  The lower bound on a keeps 448 / a
+// finite; a group of zeros gets codes of 0.
 //
-// Bound by HBM: the input once, a byte per element out, 4 bytes per group.
+// Bound by HBM: the input once, a byte per element out, 4 bytes per group; next
+// to that by instruction issue (with two IEEE divisions a lane and a test for
+// infinities per element 4096 x 8960 bf16 took 26 us, and the warps' commonest
+// stall was a ready instruction not selected).
 #include "common.cuh"
 #include "e4m3.cuh"
 
@@ -54,11 +56,10 @@ struct Share {
     else
       unpack16<float>(raw, f);
   }
-  // The largest finite magnitude (the maxima pass over NaN); `inf` says whether an
-  // infinity was among them, which is rare and settled out of the way of the
-  // others.  bf16 pairs are compared as they are: half the instructions.
-  __device__ __forceinline__ float amax(bool* inf) const {
-    float m;
+  // The largest magnitude, infinities among them (the maxima pass over NaN; NaN
+  // if there is nothing else).  bf16 pairs are compared as they are: half the
+  // instructions.
+  __device__ __forceinline__ float amax() const {
     if constexpr (VEC && sizeof(T) == 2) {
       const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
       __nv_bfloat162 a[4];
@@ -68,22 +69,21 @@ struct Share {
         a[i] = *reinterpret_cast<const __nv_bfloat162*>(&v);
       }
       const __nv_bfloat162 x = __hmax2(__hmax2(a[0], a[1]), __hmax2(a[2], a[3]));
-      m = fmaxf(__low2float(x), __high2float(x));
+      return fmaxf(__low2float(x), __high2float(x));
     } else {
       float f[kV];
       values(f);
-      m = fabsf(f[0]);
+      float m = fabsf(f[0]);
 #pragma unroll
       for (int j = 1; j < kV; ++j) m = fmaxf(m, fabsf(f[j]));
+      return m;
     }
-    *inf = m == INFINITY;
-    if (*inf) {
-      float f[kV];
-      values(f);
-      m = 0.f;
+  }
+  __device__ __forceinline__ float amax_finite() const {
+    float f[kV], m = 0.f;
+    values(f);
 #pragma unroll
-      for (int j = 0; j < kV; ++j) m = fmaxf(m, finite_abs(f[j]));
-    }
+    for (int j = 0; j < kV; ++j) m = fmaxf(m, finite_abs(f[j]));
     return m;
   }
   static __device__ __forceinline__ void store(uint8_t* row, int c0, int cols, const float* f) {
@@ -106,8 +106,16 @@ struct Share {
   }
 };
 
-// x * (448 / a) of N elements, in place (infinities go to +-448 here: times lo
-// they would become NaN).
+// 448 / a as hi + lo (2^-100 <= a).  a / 256 keeps the reciprocal's argument and
+// result inside the normal range.
+__device__ __forceinline__ void quotient(float a, float* hi, float* lo) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a * 0x1p-8f));
+  *hi = 1.75f * r;
+  *lo = fmaf(-*hi, a, kE4m3Max) * (r * 0x1p-8f);
+}
+// x * (448 / a) of N elements, in place; infinities, if there may be any, become
+// +-448 (times lo they would become NaN).
 template <int N>
 __device__ __forceinline__ void to_code_range(float* f, float a, float hi, float lo, bool inf) {
   if (inf) {
@@ -117,10 +125,6 @@ __device__ __forceinline__ void to_code_range(float* f, float a, float hi, float
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) f[j] = fmaf(f[j], hi, f[j] * lo);
-}
-__device__ __forceinline__ void quotient(float a, float* hi, float* lo) {
-  *hi = __fdiv_rn(kE4m3Max, a);
-  *lo = __fdiv_rn(fmaf(-*hi, a, kE4m3Max), a);
 }
 
 // Rows: a CTA takes 16 (fp32 and unaligned rows: 8) rows x kRowGroups groups, a
@@ -143,10 +147,15 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const Quant a) {
     in[i].load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, (g0 + i) * kGroup, cols);
 #pragma unroll
   for (int i = 0; i < kRowGroups; ++i) {
-    bool inf;
-    float m = in[i].amax(&inf);
+    float m = in[i].amax();
 #pragma unroll
     for (int o = 1; o < S::kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool inf = __any_sync(0xffffffffu, m == INFINITY);
+    if (inf) {  // rare: once more over the finite ones
+      m = in[i].amax_finite();
+#pragma unroll
+      for (int o = 1; o < S::kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    }
     m = fmaxf(m, 0x1p-100f);
     float hi, lo;
     quotient(m, &hi, &lo);
@@ -177,19 +186,25 @@ __global__ void __launch_bounds__(512) quant_blocks_kernel(const Quant a) {
     const int row = row0 + 16 * S::kRows * i;
     in[i].load(reinterpret_cast<const T*>(a.x) + (long long)row * a.stride, g * kGroup, row < a.rows ? a.cols : 0);
   }
-  bool any_inf = false;
   float m = 0.f;
+  auto block_max = [&]() {
+    m = warp_max(m);
+    if (lane == 0) wmax[warp] = m;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    bool inf;
-    m = fmaxf(m, in[i].amax(&inf));
-    any_inf |= inf;
+    for (int w = 0; w < 16; ++w) m = fmaxf(m, wmax[w]);
+  };
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) m = fmaxf(m, in[i].amax());
+  block_max();
+  const bool any_inf = m == INFINITY;
+  if (any_inf) {  // rare: once more over the finite ones
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) m = fmaxf(m, in[i].amax_finite());
+    __syncthreads();
+    block_max();
   }
-  m = warp_max(m);
-  if (lane == 0) wmax[warp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 16; ++w) m = fmaxf(m, wmax[w]);
   m = fmaxf(m, 0x1p-100f);
   float hi, lo;
   quotient(m, &hi, &lo);
