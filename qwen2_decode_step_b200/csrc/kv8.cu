@@ -146,10 +146,10 @@ __global__ void __launch_bounds__(kThreads) kv8_append_kernel(const Kv8Append a)
   if (tid == 0) *scale = s;  // every thread has read it: the barrier above
 }
 
-// One CTA reads 64 consecutive positions of one sequence (all kv heads) of K
-// or of V.  Bound by HBM: a byte in, two or four out per element.  A thread's
+// One CTA reads 64 consecutive positions of one sequence and kv head of K or of
+// V.  Bound by HBM: a byte in, two or four out per element.  A thread's
 // item is 16 bytes of output, so a warp's stores are whole lines (with 16 codes
-// an item they were 64 bytes apart: 22 us instead of 17 for 32768 positions
+// an item they were 64 bytes apart: 22 us instead of 15 for 32768 positions
 // of two heads to fp32); its loads are issued before the first store.
 template <typename T, int HD, bool VEC>
 __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8Read a, int nblk, int* err) {
@@ -167,51 +167,50 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8Read a, int
     return;
   }
   const int n = min(kBlk, a.ntok - t0) * kItemsRow;
-  for (int g = 0; g < a.nkv; ++g) {
-    const size_t head = (size_t)b * a.nkv + g;
-    const uint8_t* codes = (isv ? a.vc : a.kc) + (head * a.max_seq + start + t0) * HD;
-    const float* scale = (isv ? a.vs : a.ks) + head * nblk;
-    T* out = reinterpret_cast<T*>(isv ? a.v : a.k) + (long long)b * a.seq_stride + (long long)g * a.head_stride;
-    uint2 w[kPer];
-    float s[kPer];
+  const int g = blockIdx.z;
+  const size_t head = (size_t)b * a.nkv + g;
+  const uint8_t* codes = (isv ? a.vc : a.kc) + (head * a.max_seq + start + t0) * HD;
+  const float* scale = (isv ? a.vs : a.ks) + head * nblk;
+  T* out = reinterpret_cast<T*>(isv ? a.v : a.k) + (long long)b * a.seq_stride + (long long)g * a.head_stride;
+  uint2 w[kPer];
+  // the tile's 64 positions lie in two blocks at most
+  const int b0 = (start + t0) / kBlk, split = (b0 + 1) * kBlk - start - t0;  // rows of the tile in the first
+  const float s0 = __ldg(scale + b0), s1 = __ldg(scale + min(b0 + 1, nblk - 1));
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int it = threadIdx.x + i * kThreads;
-      w[i] = make_uint2(0u, 0u);
-      s[i] = 0.f;
-      if (it < n) {
-        if constexpr (kV == 8)
-          w[i] = __ldg(reinterpret_cast<const uint2*>(codes) + it);
-        else
-          w[i].x = __ldg(reinterpret_cast<const uint32_t*>(codes) + it);
-        s[i] = __ldg(scale + (start + t0 + it / kItemsRow) / kBlk);
-      }
+  for (int i = 0; i < kPer; ++i) {
+    const int it = threadIdx.x + i * kThreads;
+    w[i] = make_uint2(0u, 0u);
+    if (it < n) {
+      if constexpr (kV == 8)
+        w[i] = __ldg(reinterpret_cast<const uint2*>(codes) + it);
+      else
+        w[i].x = __ldg(reinterpret_cast<const uint32_t*>(codes) + it);
     }
+  }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int it = threadIdx.x + i * kThreads;
-      if (it >= n) break;
-      const int t = t0 + it / kItemsRow, d = (it % kItemsRow) * kV;
-      float f[kV];
-      e4m3x4_to_f(w[i].x, f);
-      if constexpr (kV == 8) e4m3x4_to_f(w[i].y, f + 4);
-      if (isv && a.vnan) {
+  for (int i = 0; i < kPer; ++i) {
+    const int it = threadIdx.x + i * kThreads;
+    if (it >= n) break;
+    const int t = t0 + it / kItemsRow, d = (it % kItemsRow) * kV;
+    float f[kV];
+    e4m3x4_to_f(w[i].x, f);
+    if constexpr (kV == 8) e4m3x4_to_f(w[i].y, f + 4);
+    if (isv && a.vnan) {
 #pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (isnan(f[j])) {
-            f[j] = 0.f;
-            atomicMax(a.vnan + g * HD + d + j, INT32_MAX - (start + t));
-          }
-      }
-      T* o = out + (long long)t * a.tok_stride + d;
+      for (int j = 0; j < kV; ++j)
+        if (isnan(f[j])) {
+          f[j] = 0.f;
+          atomicMax(a.vnan + g * HD + d + j, INT32_MAX - (start + t));
+        }
+    }
+    T* o = out + (long long)t * a.tok_stride + d;
 #pragma unroll
-      for (int j = 0; j < kV; ++j) f[j] *= s[i];
-      if constexpr (VEC) {
-        *reinterpret_cast<uint4*>(o) = pack16<T>(f);
-      } else {
+    for (int j = 0; j < kV; ++j) f[j] *= it / kItemsRow < split ? s0 : s1;
+    if constexpr (VEC) {
+      *reinterpret_cast<uint4*>(o) = pack16<T>(f);
+    } else {
 #pragma unroll
-        for (int j = 0; j < kV; ++j) o[j] = from_f<T>(f[j]);
-      }
+      for (int j = 0; j < kV; ++j) o[j] = from_f<T>(f[j]);
     }
   }
 }
@@ -226,7 +225,7 @@ q2_status append_t(const Kv8Append& a, bool vec, cudaStream_t st) {
 
 template <typename T, int HD>
 q2_status read_t(const Kv8Read& a, bool vec, int* err, cudaStream_t st) {
-  const dim3 grid((a.ntok + kBlk - 1) / kBlk, 2 * a.batch);
+  const dim3 grid((a.ntok + kBlk - 1) / kBlk, 2 * a.batch, a.nkv);
   Q2_LAUNCH(vec ? kv8_read_kernel<T, HD, true> : kv8_read_kernel<T, HD, false>, grid, dim3(kThreads), 0, st, true,
             a, (a.max_seq + kBlk - 1) / kBlk, err);
   return Q2_OK;
