@@ -146,8 +146,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 template <typename T>
-__device__ __forceinline__ void store_out(const Q8Lin& a, int m, int n, float y, bool bias) {
-  if (bias && a.bias) y += to_f(reinterpret_cast<const T*>(a.bias)[n]);
+__device__ __forceinline__ void store_out(const Q8Lin& a, int m, int n, float y) {
+  if (a.bias) y += to_f(reinterpret_cast<const T*>(a.bias)[n]);
   reinterpret_cast<T*>(a.out)[(size_t)m * a.N + n] = from_f<T>(y);
 }
 
@@ -455,11 +455,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
           }
-        } else if (const int m = r0 + l; m < a.M) {
+        } else {
+          // rows that do not start on 16 bytes: 32 x 32 values at a time are turned
+          // (value c of row r at (c + r) % 32: no bank conflicts), a warp stores 32
+          // neighbours of a row (a row per lane stored 32 lines at a time: 2416 x
+          // 7093 x 1104 205 us instead of 42.6)
+          float* turn = reinterpret_cast<float*>(smem + SM::kTurn + (size_t)(warp - kEpiWarp0) * 4096);
+          const int m0 = r0 + 32 * q;
 #pragma unroll
-          for (int i = 0; i < kHalf / 2; ++i) {
-            if (c0 + 2 * i < a.N) store_out<T>(a, m, c0 + 2 * i, sum[i].x, !bias_in);
-            if (c0 + 2 * i + 1 < a.N) store_out<T>(a, m, c0 + 2 * i + 1, sum[i].y, !bias_in);
+          for (int p = 0; p < kHalf / 32; ++p) {
+            const int n = c0 + 32 * p + lane;
+            const float b = a.bias && n < a.N ? to_f(reinterpret_cast<const T*>(a.bias)[n]) : 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              turn[lane * 32 + ((c + lane) & 31)] = c % 2 ? sum[16 * p + c / 2].y : sum[16 * p + c / 2].x;
+            __syncwarp();
+            if (n < a.N) {
+              T* o = reinterpret_cast<T*>(a.out) + (size_t)m0 * a.N + n;
+              const int rows = min(32, a.M - m0);
+              for (int r = 0; r < rows; ++r, o += a.N) *o = from_f<T>(turn[r * 32 + ((lane + r) & 31)] + b);
+            }
+            __syncwarp();
           }
         }
       } else {
@@ -500,10 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int r = 1; r < kClusterMax; ++r)
           if (r < a.csize) y = make_float4(y.x + v[r].x, y.y + v[r].y, y.z + v[r].z, y.w + v[r].w);
-        store_out<T>(a, m, n, y.x, true);
-        if (n + 1 < a.N) store_out<T>(a, m, n + 1, y.y, true);
-        if (n + 2 < a.N) store_out<T>(a, m, n + 2, y.z, true);
-        if (n + 3 < a.N) store_out<T>(a, m, n + 3, y.w, true);
+        store_out<T>(a, m, n, y.x);
+        if (n + 1 < a.N) store_out<T>(a, m, n + 1, y.y);
+        if (n + 2 < a.N) store_out<T>(a, m, n + 2, y.z);
+        if (n + 3 < a.N) store_out<T>(a, m, n + 3, y.w);
       }
       cluster_sync();  // no CTA leaves while another reads its tile
     }
