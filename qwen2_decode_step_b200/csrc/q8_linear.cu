@@ -37,10 +37,6 @@
 // word and the kernel carries on to its end.
 #include <cooperative_groups.h>
 
-#include <map>
-#include <mutex>
-#include <tuple>
-
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "tcgen05.cuh"
@@ -534,19 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // How many clusters of cs CTAs of `kernel` the current device runs at once; asked
-// once per kernel, size and device.
-q2_status active_clusters(const void* kernel, int cs, size_t smem, int* n) {
-  static std::mutex mu;
-  static std::map<std::tuple<int, const void*, int>, int> known;
+// once per device and size and kept in `known` (+ 1; 0: not asked yet).
+constexpr int kDevs = 64;
+using Known = std::atomic<int>[kDevs][kClusterMax + 1];
+q2_status active_clusters(const void* kernel, int cs, size_t smem, Known& known, int* n) {
   int dev = 0;
   Q2_CUDA_TRY(cudaGetDevice(&dev));
-  std::lock_guard<std::mutex> lk(mu);
-  const auto key = std::make_tuple(dev, kernel, cs);
-  const auto it = known.find(key);
-  if (it != known.end()) {
-    *n = it->second;
-    return Q2_OK;
-  }
+  if (dev < kDevs)
+    if (const int k = known[dev][cs].load(std::memory_order_relaxed)) {
+      *n = k - 1;
+      return Q2_OK;
+    }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cs);
   cfg.blockDim = dim3(kThreads);
@@ -559,7 +553,7 @@ q2_status active_clusters(const void* kernel, int cs, size_t smem, int* n) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   Q2_CUDA_TRY(cudaOccupancyMaxActiveClusters(n, kernel, &cfg));
-  known[key] = *n;
+  if (dev < kDevs) known[dev][cs].store(*n + 1, std::memory_order_relaxed);
   return Q2_OK;
 }
 
@@ -568,6 +562,7 @@ q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t
   using SM = Q8Smem<WIDE, BN, STAGES>;
   auto* kernel = q8_linear_kernel<T, WIDE, BN, STAGES>;
   static std::atomic<uint64_t> done{0};
+  static Known known;  // (zero)
   if (first_on_device(done)) {
     Q2_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SM::kTotal));
     // the register split draws on what the kernel is launched with: fewer would
@@ -598,7 +593,7 @@ q2_status launch_q8(const void* xq, const void* wq, int K, Q8Lin a, cudaStream_t
   long long best_cost = (tiles + sms - 1) / sms * (a.groups + kFixed);
   for (int cs = 2; cs <= kClusterMax && cs <= a.groups && tiles * cs <= sms; ++cs) {
     int active = 0;
-    Q2_TRY(active_clusters(reinterpret_cast<const void*>(kernel), cs, SM::kTotal, &active));
+    Q2_TRY(active_clusters(reinterpret_cast<const void*>(kernel), cs, SM::kTotal, known, &active));
     if (active < 1) continue;
     const long long cost = (tiles + active - 1) / active * ((a.groups + cs - 1) / cs + kFixed) + kJoin;
     if (cost < best_cost) {

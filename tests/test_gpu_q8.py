@@ -4,6 +4,9 @@ they can go wrong, and run together as they are used.  Written and quantised cod
 bit for bit; the bounds of the others count their roundings (q8_ref)."""
 
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -566,6 +569,114 @@ def test_two_calls_at_once_have_a_workspace_each():
                 q2.q2_kv8_attention(got[i], q[i], c[2 * i], c[2 * i + 1], sc, sc, lens[i], 0.01)
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T,lens", [(1, [65, 640, 0, 128]), (3, [65, 640, 3, 128]), (300, [700, 300, 0, 449])])
+def test_nothing_past_a_sequences_end_is_seen(dt, T, lens):
+    """NaN codes and NaN scales of every block behind a sequence's last one."""
+    nh, nkv, S, hd = 4, 2, 1000, 128
+    kc, vc, ks, vs = filled_cache(4, nkv, S, hd, 170)
+    for b, n in enumerate(lens):
+        kc[b, :, n:], vc[b, :, n:] = 255, 127
+        ks[b, :, -(-n // 64):], vs[b, :, -(-n // 64):] = math.nan, math.nan
+    q = randn(174, 4, T, nh, hd).to(DT[dt])
+    d = both(kc, vc, ks, vs)
+    out = torch.empty(4, T, nh, hd, dtype=DT[dt], device="cuda")
+    q2.q2_kv8_attention(out, q.cuda(), *d, i32(lens).cuda(), 0.09)
+    ref, bound = R.attention(q, kc, vc, ks, vs, lens, 0.09)
+    R.within(out, ref, bound, "batch")
+    for b, n in enumerate(lens):
+        if n >= T:
+            q2.q2_kv8_self_attention(out[b], q[b].cuda(), *(t[b] for t in d), n, 0.09)
+            R.within(out[b], ref[b], bound[b], f"rows of {b}")
+
+
+def test_cache_offsets_past_32_bits():
+    """The third sequence's slot of a cache of 2^24 positions starts past 2^32 bytes."""
+    B, nkv, S, hd, nh, T = 3, 1, 1 << 24, 128, 2, 3
+    kc, vc = (torch.empty(B, nkv, S, hd, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones(B, nkv, S // 64, device="cuda") for _ in range(2))
+    k, v = randn(180, B, T, nkv, hd).bfloat16(), randn(181, B, T, nkv, hd).bfloat16()
+    q = randn(182, B, T, nh, hd).bfloat16()
+    small = empty_cache(B, nkv, 64, hd)
+    R.append(small[0], small[2], k, [0, 0, 0])
+    R.append(small[1], small[3], v, [0, 0, 0])
+    for start in ([0, -1, 0], [-1, S - 64, S - 64]):  # both ends of the last slot
+        q2.q2_kv8_append(kc, vc, ks, vs, k.cuda(), v.cuda(), i32(start).cuda())
+        kr, vr = (torch.zeros(B, T, nkv, hd, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        q2.q2_kv8_read(kr, vr, kc, vc, ks, vs, i32(start).cuda())
+        for b in range(B):
+            if start[b] >= 0:
+                assert torch.equal(kr[b, :, 0].cpu().double(), R.dense(small[0], small[2])[b, 0, :T])
+                assert torch.equal(vr[b, :, 0].cpu().double(), R.dense(small[1], small[3])[b, 0, :T])
+    out = torch.empty(B, T, nh, hd, dtype=torch.bfloat16, device="cuda")
+    lens = [T, 0, T]
+    q2.q2_kv8_attention(out, q.cuda(), kc, vc, ks, vs, i32(lens).cuda(), 0.1)
+    ref, bound = R.attention(q, *small, lens, 0.1)
+    R.within(out, ref, bound)
+
+
+@pytest.mark.parametrize("N", [151936, 151935])
+def test_linear_output_past_32_bits(N):
+    """More than 2^31 outputs, in rows on 16 bytes and off them."""
+    M, K = 16400, 16
+    xq, xs = R.quantise(randn(183, M, K), 1)
+    wq, ws = R.quantise(randn(184, N, K), 128)
+    out = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    q2.q2_linear_q8(out, *both(xq, xs, wq, ws))
+    rows = [0, 2 ** 31 // N, 2 ** 31 // N + 1, M - 1]
+    ref, bound = R.linear(xq[rows], xs[:, rows], wq, ws, None, torch.bfloat16)
+    R.within(out[rows], ref, bound)
+
+
+@pytest.mark.parametrize("br", [1, 128])
+def test_quantize_past_32_bits(br):
+    rows, cols = (1 << 20) + 131, 2064
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(185))
+    codes = torch.empty(rows, cols, dtype=torch.uint8, device="cuda")
+    G = -(-cols // 128)
+    scales = torch.empty((G, rows) if br == 1 else (-(-rows // 128), G), device="cuda")
+    q2.q2_quantize_q8(codes, scales, x, br)
+    first = rows // 128 * 128 - 128
+    c, s = R.quantise(x[first:].cpu(), br)
+    same_codes(codes[first:], c, "codes")
+    assert torch.equal(scales[:, first:].cpu() if br == 1 else scales[first // 128:].cpu(), s)
+
+
+FIRST = """
+import torch, qwen2_decode_step_b200 as q2
+z = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device="cuda")
+u8, bf = torch.uint8, torch.bfloat16
+cache = z(2, 2, 700, 128, dt=u8), z(2, 2, 700, 128, dt=u8), z(2, 2, 11), z(2, 2, 11)
+k, start, lens = z(2, 300, 2, 128, dt=bf) + 1, z(2, dt=torch.int32), z(2, dt=torch.int32) + 300
+o, r, one = z(2, 300, 4, 128, dt=bf), z(2, 300, 2, 128, dt=bf), z(300, 4, 128, dt=bf)
+q = z(2, 300, 4, 128, dt=bf)
+x, c, s, wc, ws, y = z(70, 256, dt=bf) + 2, z(70, 256, dt=u8), z(2, 70), z(256, 256, dt=u8), z(2, 2), z(70, 256)
+y1 = z(1, 256)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    q2.q2_kv8_append(*cache, k, k, start)
+    q2.q2_kv8_read(r, torch.empty_like(r), *cache, start)
+    q2.q2_kv8_attention(o, q, *cache, lens, 0.1)
+    q2.q2_kv8_self_attention(one, q[0], *(t[0] for t in cache), 300, 0.1)
+    q2.q2_quantize_q8(c, s, x)
+    q2.q2_quantize_q8(wc, ws, torch.cat([x] * 4)[:256], 128)
+    q2.q2_linear_q8(y, c, s, wc, ws)
+    q2.q2_linear_q8(y1, c[:1], s[:, :1].contiguous(), wc, ws)
+g.replay()
+torch.cuda.synchronize()
+assert bool((r == 1).all()) and bool((o == 1).all()) and bool((one == 1).all())
+assert bool(((y - 1024).abs() < 1e-2).all()) and torch.equal(y1, y[:1])
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """Attributes, symbols and occupancies are asked for inside the capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_workspace_too_small_is_refused():
