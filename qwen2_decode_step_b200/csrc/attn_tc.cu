@@ -205,11 +205,16 @@ struct AttnTc {
   const int* vnan;  // null, or [nkv][hd]: INT32_MAX - the first position with a NaN of V in that dim (0: none)
 };
 
-// Eight dims of the row at position pos: NaN where one of V's lies at or before it.
-__device__ __forceinline__ void mark_nan(const int* vnan, int pos, float* f) {
+// Eight dims of the row at position pos: NaN where one of V's lies at or before it,
+// and everywhere in a row whose scores leave no sum (`none`: its query is not
+// finite, or a key range's scores are all NaN).
+__device__ __forceinline__ void mark_nan(const int* vnan, int pos, bool none, float* f) {
+  const int4 lo = __ldg(reinterpret_cast<const int4*>(vnan)), hi = __ldg(reinterpret_cast<const int4*>(vnan) + 1);
+  const int first[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  const int from = none ? 0 : INT32_MAX - pos;  // (a first position of `pos` or before)
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if (INT32_MAX - __ldg(vnan + i) <= pos) f[i] = NAN;
+    if (first[i] >= from) f[i] = NAN;
 }
 
 // A slot: O (fp32, [row][dim]), then m and l of each row.
@@ -483,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float f[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(ov[e + t]) * inv;
-            if (a.vnan) mark_nan(a.vnan + (size_t)kvh * kHD + cb + 32 * c + e, a.pos0 + row, f);
+            if (a.vnan)
+              mark_nan(a.vnan + (size_t)kvh * kHD + cb + 32 * c + e, a.pos0 + row, m_run == -INFINITY || isnan(lr), f);
             *reinterpret_cast<uint4*>(out + 32 * c + e) = pack16<bf16>(f);
           }
         }
@@ -524,7 +530,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < a.ts; ++k) {
           const float* sk = a.part + (size_t)(k * n_tail + t) * kSlotFloats;
           const float mk = __ldcg(sk + kQB * kHD + r);
-          if (mk == -INFINITY) continue;  // the row sees no key in this range
+          if (mk == -INFINITY) {  // the row sees no key in this range (or NaN scores alone)
+            if (a.vnan) ll += __ldcg(sk + kQB * kHD + kQB + r);  // 0 or NaN
+            continue;
+          }
           const float w = exp2f(mk - mm);
           ll += w * __ldcg(sk + kQB * kHD + kQB + r);
           const float4* src = reinterpret_cast<const float4*>(sk + (size_t)r * kHD + cb);
@@ -544,7 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float f[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) f[u] = o[e + u] * inv;
-            if (a.vnan) mark_nan(a.vnan + (size_t)kvh * kHD + cb + e, a.pos0 + row, f);
+            if (a.vnan)
+              mark_nan(a.vnan + (size_t)kvh * kHD + cb + e, a.pos0 + row, mm == -INFINITY || isnan(ll), f);
             *reinterpret_cast<uint4*>(out + e) = pack16<bf16>(f);
           }
         }

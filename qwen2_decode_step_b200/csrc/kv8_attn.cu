@@ -459,7 +459,9 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
       // 2^k brings the row's largest magnitude to [256, 512)
       const int k = m > 0.f ? min(126, 127 + 8 - (int)(__float_as_uint(m) >> 23)) : 0;
-      const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+      // (an infinite query leaves nothing but infinite and NaN scores: NaN, also
+      // where all of them are -inf and no weight would be left)
+      const float up = m < INFINITY ? __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
       const float down = sl2 * __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll
       for (int j = 0; j < kW; ++j) {

@@ -389,6 +389,45 @@ def test_attention_with_large_small_and_zero_queries(dt):
         R.within(out, ref, bound, f"scale {scale}")
 
 
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("rows", [1, 4, 40, 260])
+@pytest.mark.parametrize("x", [math.inf, -math.inf, math.nan])
+def test_attention_with_queries_that_are_not_finite(dt, rows, x):
+    """They make their own rows NaN, also where every score is -inf, and no others."""
+    S, hd, nh, nkv = 300, 128, 4, 2
+    kc, vc, ks, vs = filled_cache(1, nkv, S, hd, 106)
+    kc[..., 3] |= 128   # (q[3] = inf: -inf everywhere)
+    kc[..., 3] &= 0xfe  # (no NaN code)
+    kc[..., 5] &= 0x7e
+    q = randn(109, 1, rows, nh, hd).to(DT[dt])
+    q[0, 0, 0, 3], q[0, rows // 2, 2, 5], q[0, rows - 1, 3, 100] = x, x, x
+    d = both(kc, vc, ks, vs)
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    out = torch.empty(1, rows, nh, hd, dtype=DT[dt], device="cuda")
+    q2.q2_kv8_attention(out, q.cuda(), *d, i32([S]).cuda(), 0.09)
+    R.within(out, ref, bound, "batch")
+    q2.q2_kv8_self_attention(out[0], q[0].cuda(), *(t[0] for t in d), S, 0.09)
+    R.within(out, ref, bound, "rows")
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("rows", [1, 5, 300])
+def test_attention_over_a_stretch_of_nan_keys(dt, rows):
+    """Whole key ranges of NaN, as a split of the keys may hand one to a CTA."""
+    S, hd, nh, nkv = 2000, 128, 4, 2
+    kc, vc, ks, vs = filled_cache(1, nkv, S, hd, 110)
+    kc[0, 0, 400:1300] = 127
+    q = randn(114, 1, rows, nh, hd).to(DT[dt])
+    d = both(kc, vc, ks, vs)
+    out = torch.empty(1, rows, nh, hd, dtype=DT[dt], device="cuda")
+    for n in (S, 690):  # all rows see them; the first of the 300 do not
+        ref, bound = R.attention(q, kc, vc, ks, vs, [n], 0.09)
+        q2.q2_kv8_attention(out, q.cuda(), *d, i32([n]).cuda(), 0.09)
+        R.within(out, ref, bound, "batch")
+        q2.q2_kv8_self_attention(out[0], q[0].cuda(), *(t[0] for t in d), n, 0.09)
+        R.within(out, ref, bound, "rows")
+
+
 def test_attention_is_the_same_every_time_and_beside_other_sequences():
     S, hd, nh, nkv, B = 3000, 128, 12, 2, 5
     g = torch.Generator(device="cuda").manual_seed(3)
