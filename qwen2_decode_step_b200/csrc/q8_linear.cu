@@ -284,7 +284,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kTwo = kNCh > 1 ? 2 : 1;             // TMEM loads in flight
     constexpr int kWs = WIDE && BN == 192 ? 3 : 1;     // weight scales of the warp's columns: 96 may straddle a block
     constexpr int kV = Storage<T>::kVec;
-    constexpr int kAhead = 2;                          // groups whose scales are read at a time
+    // Weight scales: of 256 columns by lane (32 groups' lie next to each other, a
+    // lane reads one and hands it to the others at its group), and the loop in steps
+    // of one group; 4096 x 17920 x 1536 131 -> 118 us, x 4096 308 -> 292.  Of fewer
+    // columns by every lane at each group, in steps of two: by lane 192 columns
+    // took 74-80 us instead of 65-72 (4096 x 1536 x 8960), 128 columns 32 instead
+    // of 30 (1000 x 4096 x 4096 fp32), 64 tokens the same.
+    constexpr bool kShare = WIDE && BN == 256;
+    constexpr int kAhead = kShare ? 1 : 2;             // groups of a step; the next step's scales are read ahead
     const int q = warp & 3, half = (warp - kEpiWarp0) / 4;
     const int l = 32 * q + lane;                       // this thread's TMEM lane
     const uint32_t tbase = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * kHalf);
@@ -296,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // stored.  Rows and groups outside are held to the last one (their products
     // are not stored or not formed), so that the loads need no predicate.
     float xs[kAhead], ws[kAhead][kWs];
+    [[maybe_unused]] float wl = 0.f, wl_next = 0.f;  // kShare: of this lane's group of 32, of the next 32
     const float* xp;
     const float* wp[kWs];
     auto seek = [&](const TileWalk& w) {
@@ -313,13 +321,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int at = min(g + u, g1 - 1);
         x[u] = __ldg(xp + (size_t)at * a.M);
 #pragma unroll
-        for (int j = 0; j < kWs; ++j) w[u][j] = __ldg(wp[j] + at);
+        for (int j = 0; j < kWs; ++j) w[u][j] = kShare ? 0.f : __ldg(wp[j] + at);
       }
     };
+    auto load_lanes = [&](int g) { return __ldg(wp[0] + min(g + lane, g1 - 1)); };
     TileWalk w(first, step, a.lane_tiles);
     if (w.t < a.tiles) {
       seek(w);
       load_scales(xs, ws, g0);
+      if constexpr (kShare) wl = load_lanes(g0);
     }
     while (w.t < a.tiles) {
       const int r0 = w.lt * kLanes, c0 = w.ct * BN + half * kHalf;
@@ -342,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int gg = g0; gg < g1; gg += kAhead) {
         float xn[kAhead], wn[kAhead][kWs];
         load_scales(xn, wn, gg + kAhead);
+        if constexpr (kShare)
+          if (((gg - g0) & 31) == 0 && gg + 32 < g1) wl_next = load_lanes(gg + 32);
 #pragma unroll
         for (int ahead = 0; ahead < kAhead; ++ahead) {
           if (gg + ahead >= g1) break;
@@ -362,7 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < kTwo; ++u) {
               if (c + u >= kNCh) continue;
-              const float f = xs[ahead] * ws[ahead][kWs > 1 ? c + u : 0];
+              const float f = xs[ahead] * (kShare ? __shfl_sync(0xffffffffu, wl, (gg - g0) & 31)
+                                                  : ws[ahead][kWs > 1 ? c + u : 0]);
 #pragma unroll
               for (int i = 0; i < kCh / 2; ++i) {
                 const int at = (c + u) * kCh / 2 + i;
@@ -385,11 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kWs; ++j) ws[u][j] = wn[u][j];
         }
+        if constexpr (kShare)
+          if (((gg + 1 - g0) & 31) == 0) wl = wl_next;
       }
       w.next();
       if (w.t < a.tiles) {
         seek(w);
         load_scales(xs, ws, g0);
+        if constexpr (kShare) wl = load_lanes(g0);
       }
       if (a.csize > 1) {
         // every load of the ring has been consumed by a completed MMA

@@ -557,7 +557,7 @@ def test_linear_of_zero_codes_is_the_bias():
 @pytest.mark.parametrize("dt", DT)
 @pytest.mark.parametrize("M,N,K", [(1, 17920, 1536), (4, 1536, 8960), (61, 2048, 1536), (700, 1536, 1536),
                                    (1025, 2100, 8960), (4096, 1536, 256), (4001, 1544, 144), (2300, 4104, 272),
-                                   (2500, 3001, 128)])
+                                   (2500, 3001, 128), (2500, 3000, 4096), (2500, 3001, 4112), (2500, 3000, 8960)])
 def test_linear_at_the_layers_sizes(dt, M, N, K):
     """Full-size products, the whole output against a 64-bit product on the GPU."""
     g = torch.Generator(device="cuda").manual_seed(6)
