@@ -228,8 +228,9 @@ q2_status q2_kv8_read(void* k, void* v, const void* kc, const void* vc, const fl
  * elements of a token contiguous; q_strides as k_strides above), out dense and
  * 16-byte aligned; scores, softmax and sums in fp32.  A row that sees no key (a sequence of
  * length <= 0, or lens[b] < ntok) is zero; lens[b] past max_seq: zero rows and
- * Q2_ERR_CAPACITY in the device error word.  Codes past lens[b] may hold
- * anything.  nh / nkv <= 8.
+ * Q2_ERR_CAPACITY in the device error word.  Codes and scales past lens[b] may
+ * hold anything.  A query row that is not finite, or sees a NaN of K, is NaN in
+ * every dimension, one that sees a NaN of V in that dimension.  nh / nkv <= 8.
  * workspace: device memory of at least q2_kv8_attention_workspace() bytes,
  * 256-byte aligned, contents ignored (NULL where that is 0); calls that may
  * overlap on the GPU need one each. */
