@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ahead = 0; ahead < kAhead; ++ahead) {
           if (gg + ahead >= g1) break;
           if (!tc_wait_asleep(&acc_full[acc], aph) && lane == 0) atomicOr(a.err, kErrTimeout);
+          __syncwarp();  // (each lane waited for itself: the loads below take whole warps)
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < kNCh; c += kTwo) {
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n + 2 < a.N) store_out<T>(a, m, n + 2, y.z);
         if (n + 3 < a.N) store_out<T>(a, m, n + 3, y.w);
       }
+      __syncwarp();    // (lanes skip what lies outside the output: the barrier takes whole warps)
       cluster_sync();  // no CTA leaves while another reads its tile
     }
   }
