@@ -199,6 +199,12 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The CTA's barrier inside the item loop: it takes whole warps, whose lanes may
+// just have done unequal work.
+__device__ __forceinline__ void cta_sync() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 // Which of the four codes of a word are NaN, as 0xff bytes.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) {
   return __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -511,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         vs_n = __ldg(vsp + (key0 + kw * kKeys) / kBlk);
       }
       if (!tc_wait_asleep(&full[slot0 + use_s], use_ph) && lane == 0) atomicOr(a.err, kErrTimeout);
+      __syncwarp();  // (each lane waited for itself: the MMAs take whole warps)
       uint8_t* tile = ring + (size_t)use_s * SM::kSlot;
       const uint32_t kt = smem_u32(tile), vt = kt + (uint32_t)SM::kTile;
       if (m0 < rows) {  // (three warps' rows of four: the last has none)
@@ -800,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
 
     // ---- the item's rows: each warp's normalised output, maximum and sum, over
     // its share of the slots (all consumed, once every warp is here)
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    cta_sync();
     float* Ow = reinterpret_cast<float*>(smem + (size_t)warp * SM::kShare);
 #pragma unroll
     for (int h = 0; h < NT; ++h)
@@ -828,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
           MLw[2 * (kRows * warp + r) + 1] = l;
         }
       }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    cta_sync();
     // ---- joined over the key-splitting warps: to the output, or to this CTA's
     // first (slot 0: the item began at or before the run) or last partial.  First
     // each row's weights, over its m and l
@@ -861,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
     }
     if (tid == 0 && w.at == 0 && !a.whole)
       a.cut[w.e * a.nkv + w.g] = make_cut((u + w.nu - 1) / run - (int)blockIdx.x + 1, blockIdx.x, u != u0 ? 1 : 0);
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    cta_sync();
 #pragma unroll 2
     for (int i = tid; i < here * (HD / 4); i += kThreads) {
       const int rr = i / (HD / 4), d = i % (HD / 4) * 4;
@@ -892,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
     w.at += n;
     if (u < u1) {
       fence_async_smem();  // the rows before the slots' next copies
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      cta_sync();
       w.next_item(a);
     }
   }

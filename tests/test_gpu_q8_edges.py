@@ -36,3 +36,22 @@ def test_linear_split_over_a_cluster_with_remainder_tiles(dt, M, N, K):
     ref, bound = R.linear(xq, xs, wq, ws, bias, DT[dt])
     R.within(outs[0], ref, bound, "linear")
     assert torch.equal(outs, outs[:1].expand_as(outs))
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("hd,nh,nkv,T", [(128, 7, 1, 1), (128, 6, 2, 5), (64, 5, 1, 3), (32, 3, 3, 9), (128, 5, 1, 14)])
+def test_attention_of_odd_rows_and_many_items_a_run(dt, hd, nh, nkv, T):
+    """Several items in a CTA's run, rows that fill neither a warp's tiles nor the CTA; many launches
+    behind one another."""
+    S, lens = 4100, [T, 33, 700, 0, 96, 4100, T + 1, 61, 2047, 350, 31, 64]
+    B = len(lens)
+    kc, vc, ks, vs = filled_cache(B, nkv, S, hd, 310, spread=0.7)
+    q = randn(314, B, T, nh, hd).to(DT[dt])
+    scale = 1.0 / math.sqrt(hd)
+    d = both(q, kc, vc, ks, vs, i32(lens))
+    outs = torch.full((20, B, T, nh, hd), 7.0, dtype=DT[dt], device="cuda")
+    for o in outs:
+        q2.q2_kv8_attention(o, *d, scale)
+    ref, bound = R.attention(q, kc, vc, ks, vs, lens, scale)
+    R.within(outs[0], ref, bound, "attention")
+    assert torch.equal(outs, outs[:1].expand_as(outs))
