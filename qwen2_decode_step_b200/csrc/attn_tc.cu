@@ -633,8 +633,9 @@ void attn_tc_plan(int rows, int pos0, int nh, int sms, bool split_ok, int* n_who
   if (*ts > 1) *n_whole = items - n_tail;
 }
 
+// (a.scale > 0: the kernel takes a row's largest score, and masks, before it scales)
 bool attn_tc_supported(const AttnRows& a, int dtype) {
-  return dtype == Q2_BF16 && a.hd == kHD && !a.seq_is_row && a.lens == nullptr && a.row_step == 1 &&
+  return dtype == Q2_BF16 && a.scale > 0.f && a.hd == kHD && !a.seq_is_row && a.lens == nullptr && a.row_step == 1 &&
          a.nkv > 0 && a.nh % a.nkv == 0 && a.rows >= 16 && a.base >= 1 && a.fixed_seq >= 0 &&
          (a.q_row_stride % 8) == 0 && (kv_head_major(a) || kv_token_major(a)) && (a.out_row_stride % 8) == 0 &&
          (reinterpret_cast<uintptr_t>(a.q) & 15) == 0 && (reinterpret_cast<uintptr_t>(seq_k(a)) & 15) == 0 &&

@@ -1263,8 +1263,9 @@ q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const 
   a.nblk = (int)((max_seq + kBlk - 1) / kBlk);
   a.scale = scale;
   a.out = out;
-  // (the tcgen05 attention reads q and writes out in 16-byte pieces)
-  if (use_tc(seqlen, nh / nkv, hd, dtype) &&
+  // (the tcgen05 attention reads q and writes out in 16-byte pieces, and takes the
+  // largest score, and masks, before it scales: right for a positive scale alone)
+  if (use_tc(seqlen, nh / nkv, hd, dtype) && scale > 0.f &&
       ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) == 0)
     return attn_tc(a, kc, vc, workspace, workspace_bytes, as_stream(stream));
   return attn(a, (int)hd, dtype, kc, vc, workspace, workspace_bytes, as_stream(stream));
@@ -1283,7 +1284,7 @@ q2_status q2_kv8_attention_workspace(size_t batch, size_t ntok, size_t total_len
   *bytes = split_plan(batch, ntok, nh, nkv, hd, max_seq, dtype).bytes;
   if (total_len && use_tc(ntok, nh / nkv, hd, dtype)) {
     const size_t tc = tc_plan(ntok, total_len, nh, nkv).bytes;
-    if (tc > *bytes) *bytes = tc;  // (either path, as the alignment of q and out has it)
+    if (tc > *bytes) *bytes = tc;  // (either path, as the scale and the alignment of q and out have it)
   }
   return Q2_OK;
 }

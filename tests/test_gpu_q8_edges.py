@@ -55,3 +55,30 @@ def test_attention_of_odd_rows_and_many_items_a_run(dt, hd, nh, nkv, T):
     ref, bound = R.attention(q, kc, vc, ks, vs, lens, scale)
     R.within(outs[0], ref, bound, "attention")
     assert torch.equal(outs, outs[:1].expand_as(outs))
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("rows", [6, 200, 260])
+@pytest.mark.parametrize("scale", [-0.05, 0.0, -3.0])
+def test_self_attention_with_scales_that_are_not_positive(dt, rows, scale):
+    """200 rows of two heads stay below the tcgen05 attention's sizes, 260 reach them."""
+    kc, vc, ks, vs = filled_cache(1, 1, 300, 128, 320)
+    q = randn(324, 1, rows, 2, 128).to(DT[dt])
+    d = both(kc, vc, ks, vs)
+    out = torch.empty(rows, 2, 128, dtype=DT[dt], device="cuda")
+    q2.q2_kv8_self_attention(out, q[0].cuda(), *(t[0] for t in d), 290, scale)
+    ref, bound = R.attention(q, kc, vc, ks, vs, [290], scale)
+    R.within(out, ref[0], bound[0], "self attention")
+
+
+@pytest.mark.parametrize("rows", [5, 100, 260])
+@pytest.mark.parametrize("scale", [-0.05, 0.0])
+def test_dense_self_attention_with_scales_that_are_not_positive(rows, scale):
+    """The bf16 attention that shares the tcgen05 kernel, over the values of an 8-bit cache."""
+    kc, vc, ks, vs = filled_cache(1, 2, 290, 128, 325)
+    k, v = (R.dense(c, s)[0].transpose(0, 1).bfloat16().contiguous().cuda() for c, s in ((kc, ks), (vc, vs)))
+    q = randn(329, 1, rows, 4, 128).bfloat16()
+    out = torch.empty(rows, 4, 128, dtype=torch.bfloat16, device="cuda")
+    q2.q2_self_attention(out, q[0].cuda(), k, v, scale)
+    ref, bound = R.attention(q, kc, vc, ks, vs, [290], scale)
+    R.within(out, ref[0], bound[0], "dense")
