@@ -879,12 +879,12 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
           const int wp = rr / kRows + k * a.nm, lr = rr % kRows;
           const float e = MLw[2 * (kRows * wp + lr)];
           const float4 v = *reinterpret_cast<const float4*>(smem + (size_t)wp * SM::kShare + (lr * SM::kRowF + d) * 4);
-          if (e != 0.f) {  // (a part that saw no key; NaN is kept)
-            y.x = fmaf(e, v.x, y.x);
-            y.y = fmaf(e, v.y, y.y);
-            y.z = fmaf(e, v.z, y.z);
-            y.w = fmaf(e, v.w, y.w);
-          }
+          // (no weight is skipped: a part that saw no key has outputs of 0, and a NaN
+          // of V counts also where the part's weight underflows)
+          y.x = fmaf(e, v.x, y.x);
+          y.y = fmaf(e, v.y, y.y);
+          y.z = fmaf(e, v.z, y.z);
+          y.w = fmaf(e, v.w, y.w);
         }
       if (whole) {
         const int r = w.mg * a.irows + rr, t = row_tok(a, r);
@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a)
       y = make_float4(y.x * keep, y.y * keep, y.z * keep, y.w * keep);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (i0 + k * pg < n && w[k].y != 0.f) {  // (a part that saw no key; NaN is kept)
+        if (i0 + k * pg < n) {  // (no weight is skipped, as above)
           const float e = w[k].y * ex2(w[k].x - ms);
           W += e;
           y.x = fmaf(e, v[k].x, y.x);
@@ -983,7 +983,6 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a)
         W = 0.f;
         for (int k = 0; k < pg; ++k) {
           const float2 u = s_ml[grp + k];
-          if (u.y == 0.f) continue;
           const float e = ex2(u.x - ms);
           const float4 v = s_o[tid + k * kLanes];
           W = fmaf(e, u.y, W);

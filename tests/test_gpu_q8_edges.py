@@ -82,3 +82,27 @@ def test_dense_self_attention_with_scales_that_are_not_positive(rows, scale):
     q2.q2_self_attention(out, q[0].cuda(), k, v, scale)
     ref, bound = R.attention(q, kc, vc, ks, vs, [290], scale)
     R.within(out, ref[0], bound[0], "dense")
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("S", [500, 3000])  # an item whole, and cut into runs
+@pytest.mark.parametrize("nh,T", [(4, 1), (6, 3), (8, 5), (4, 40), (4, 200)])
+def test_a_nan_of_v_stays_where_its_weight_is_nothing(dt, S, nh, T):
+    """A key whose weight underflows next to another part's is seen all the same."""
+    hd, nkv = 128, 1
+    k = 0.01 * randn(330, 1, S, nkv, hd)
+    k[0, 130] = 8.0                       # its score lies 700 above the others
+    kc, vc, ks, vs = empty_cache(1, nkv, S, hd)
+    R.append(kc, ks, k, [0])
+    R.append(vc, vs, randn(331, 1, S, nkv, hd), [0])
+    for i, p in enumerate([2, 37, 69, 100, 129, 140, 163, 200, 230, 260, 290]):
+        vc[0, 0, p, 3 + 5 * i] = 127
+    q = (0.9 + 0.1 * torch.rand(1, T, nh, hd, generator=torch.Generator().manual_seed(332))).to(DT[dt])
+    d = both(kc, vc, ks, vs)
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.7)
+    assert int(torch.isnan(ref).sum()) == 11 * T * nh
+    out = torch.empty(1, T, nh, hd, dtype=DT[dt], device="cuda")
+    q2.q2_kv8_attention(out, q.cuda(), *d, i32([S]).cuda(), 0.7)
+    R.within(out, ref, bound, "batch")
+    q2.q2_kv8_self_attention(out[0], q[0].cuda(), *(t[0] for t in d), S, 0.7)
+    R.within(out, ref, bound, "rows")
