@@ -61,6 +61,12 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasMax = 512;
 constexpr float kPBias = 6.f, kGrow = 8.f;      // p <= 2^(6 + 8) in fp16, see softmax
+// fp32: the low fp16 part of a query element or probability is kept times kLow, in
+// sums of its own, so that fp16's smallest step, 2^-24, costs 2^-37 and not 2^-25
+// (a key holding nearly all weight over 32767 others of 2^-31 each: they were lost
+// from the products and stayed in the sum).  The high part's error is at most 2^2
+// (p below 2^14), times kLow 2^14.
+constexpr float kLow = 0x1p12f;
 
 struct Kv8Attn {
   const void* q;
@@ -482,8 +488,8 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
           qb[0][h][j][1] = q1;
           if constexpr (kWide) {
             const float2 y0 = unpack_f16x2(q0), y1 = unpack_f16x2(q1);
-            qb[1][h][j][0] = pack_f16x2(x0 - y0.x, x1 - y0.y);
-            qb[1][h][j][1] = pack_f16x2(x2 - y1.x, x3 - y1.y);
+            qb[1][h][j][0] = pack_f16x2((x0 - y0.x) * kLow, (x1 - y0.y) * kLow);
+            qb[1][h][j][1] = pack_f16x2((x2 - y1.x) * kLow, (x3 - y1.y) * kLow);
           }
         }
       }
@@ -574,8 +580,8 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
               for (int i = 0; i < 4; ++i) {
                 float sum = t[0][h][i];
 #pragma unroll
-                for (int x2 = 1; x2 <= kChains; ++x2) sum += t[x2][h][i];
-                s[h][m][i] = sum;
+                for (int x2 = 1; x2 < kChains; ++x2) sum += t[x2][h][i];
+                s[h][m][i] = fmaf(t[kChains][h][i], 1.f / kLow, sum);
               }
           }
         } else if constexpr (SM::kQShared) {  // the row tiles are side by side: one key tile at a time
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
               pb[0][h][m][i] = turn8x8(hi);
               if constexpr (kWide) {
                 const float2 y = unpack_f16x2(hi);
-                pb[1][h][m][i] = turn8x8(pack_f16x2(p0 - y.x, p1 - y.y));
+                pb[1][h][m][i] = turn8x8(pack_f16x2((p0 - y.x) * kLow, (p1 - y.y) * kLow));
               }
             }
         }
@@ -768,12 +774,12 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
                                     e4m3x2_to_f16x2((uint16_t)(y1 & 0xffffu)), e4m3x2_to_f16x2((uint16_t)(y1 >> 16))};
 #pragma unroll
             for (int h = 0; h < NT; ++h) {
-              if constexpr (kWide) {  // a sum of its own, added with rounding (as the scores)
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(t, va, pb[kTerms - 1][h][kk][0], pb[kTerms - 1][h][kk][1]);
+              if constexpr (kWide) {  // sums of their own, added with rounding (as the scores)
+                float t[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(low, va, pb[kTerms - 1][h][kk][0], pb[kTerms - 1][h][kk][1]);
                 mma_f16(t, va, pb[0][h][kk][0], pb[0][h][kk][1]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[h][c][j] += t[j];
+                for (int j = 0; j < 4; ++j) o[h][c][j] += fmaf(low[j], 1.f / kLow, t[j]);
               } else {
                 mma_f16(o[h][c], va, pb[0][h][kk][0], pb[0][h][kk][1]);
               }

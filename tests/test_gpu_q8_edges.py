@@ -106,3 +106,54 @@ def test_a_nan_of_v_stays_where_its_weight_is_nothing(dt, S, nh, T):
     R.within(out, ref, bound, "batch")
     q2.q2_kv8_self_attention(out[0], q[0].cuda(), *(t[0] for t in d), S, 0.7)
     R.within(out, ref, bound, "rows")
+
+
+@pytest.mark.parametrize("nats", [10.0, 21.0, 22.0, 25.0])
+def test_fp32_weights_far_below_a_dominant_key(nats):
+    """One key holds nearly all the weight and has a V of 0 or 1, 32767 others share the rest.
+
+    In units of the dominant weight a small one is e^-nats, known to 2^-43 (the fp16 parts' floor,
+    2^-37, of probabilities of at least 2^6); the rest as q8_ref.attention counts it, the sums over
+    n keys with 2 sqrt(n) steps each."""
+    n, hd, nh, T = 32768, 32, 8, 2048
+    kc, vc = (torch.zeros(1, n, hd, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones(1, n // 64, device="cuda") for _ in range(2))
+    one = 7 << 3
+    kc[0, 7] = one                        # a score of nats; every other one is 0
+    g = torch.Generator(device="cuda").manual_seed(340)
+    vc[0, :, :16] = one
+    vc[0, :, 16:] = torch.randint(0, 120, (n, 16), generator=g, dtype=torch.uint8, device="cuda")
+    vc[0, 7, ::2] = 0
+    q = torch.ones(T, nh, hd, device="cuda")
+    out = torch.empty_like(q)
+    q2.q2_kv8_self_attention(out, q, kc, vc, ks, vs, n, nats / hd)
+    v = R.value(vc[0]).cuda()
+    w = math.exp(-float(torch.tensor(nats / hd)) * hd)
+    seen = torch.arange(n - T + 1, n + 1, device="cuda")
+    sums = (v.cumsum(0) - v[7])[seen - 1]
+    ref = (v[7] + w * sums) / (1 + w * (seen - 1))[:, None]
+    ds = (hd * 2.0 ** -23 + 4 * 2.0 ** -24) * nats
+    rel = 2 * ds + 2.0 ** -21 + 4 * math.sqrt(n) * 2.0 ** -23 + 8 * 2.0 ** -24
+    bound = rel * ref + 2.0 ** -43 * (sums + ref * seen[:, None])
+    for h in range(nh):
+        R.within(out[:, h], ref.cpu(), bound.cpu(), f"head {h}")
+
+
+def test_fp32_query_elements_far_below_the_largest():
+    """The row's largest element meets keys of 0; what decides is 2^-34 of it, known to 2^-45."""
+    S, hd, nh, nkv = 300, 64, 4, 2
+    k = 2.0 ** 14 * randn(345, 1, S, nkv, hd)
+    k[..., 0] = 0
+    kc, vc, ks, vs = empty_cache(1, nkv, S, hd)
+    R.append(kc, ks, k, [0])
+    R.append(vc, vs, randn(346, 1, S, nkv, hd), [0])
+    for T in (1, 5):
+        q = 2.0 ** -14 * randn(347, 1, T, nh, hd)
+        q[..., 0] = 2.0 ** 20
+        out = torch.empty(1, T, nh, hd, device="cuda")
+        q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([S]).cuda(), 0.2)
+        ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.2)
+        # an element's error, 2^-45 of 2^20, moves a score by at most e, and a weight by e^2e
+        e = 2.0 ** -25 * float(R.dense(kc, ks).abs().sum(-1).max()) * 0.2
+        A = R.attention(q, kc, vc & 127, ks, vs, [S], 0.2)[0]
+        R.within(out, ref, bound + math.expm1(2 * e) * A)
