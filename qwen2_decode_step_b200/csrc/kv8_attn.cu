@@ -61,6 +61,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasMax = 512;
 constexpr float kPBias = 6.f, kGrow = 8.f;      // p <= 2^(6 + 8) in fp16, see softmax
+// References above this (in powers of two) lie a sixteenth or more off their own
+// exact product: from here on every score is rounded before the reference is taken
+// from it, so that the difference is exact and the bound on p holds (below it one
+// rounding of the difference, small where p is large).
+constexpr float kCoarse = 0x1p20f;
 // fp32: the low fp16 part of a query element or probability is kept times kLow, in
 // sums of its own, so that fp16's smallest step, 2^-24, costs 2^-37 and not 2^-25
 // (a key holding nearly all weight over 32767 others of 2^-31 each: they were lost
@@ -514,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
       l_run[h][0] = l_run[h][1] = 0.f;
     }
     float unit = 0.f, unit_max = 0.f;
+    bool coarse = false;  // a row's reference is large (the same in every lane)
 
     for (int x = kg; x < n; x += kw) {
       const int key0 = (w.at + x) * kKeys;
@@ -687,10 +693,11 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
                   if (hidden(h, j, m, i)) v[m][i] = -INFINITY;
             }
             top[h][j] = fmaxf(fmaxf(v[0][0], v[0][1]), fmaxf(v[1][0], v[1][1]));
-            grow |= top[h][j] > m_run[h][j] + kGrow;
+            grow |= top[h][j] - m_run[h][j] > kGrow;
           }
         if (__any_sync(0xffffffffu, grow)) {
           float move[NT][2];  // of the output: to the new reference and unit
+          bool large = false;
 #pragma unroll
           for (int o2 = 4; o2 < 32; o2 <<= 1)
 #pragma unroll
@@ -706,7 +713,9 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
               move[h][j] = ratio * alpha;
               l_run[h][j] *= alpha;
               m_run[h][j] = mn;
+              large |= mn != -INFINITY && fabsf(mn) > kCoarse;
             }
+          coarse = __any_sync(0xffffffffu, large);
 #pragma unroll
           for (int h = 0; h < NT; ++h)
 #pragma unroll
@@ -721,13 +730,22 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
 #pragma unroll
               for (int j = 0; j < 4; ++j) o[h][c][j] *= ratio;
         }
+        if (coarse) {  // (in one place: a branch at each row cost four row tiles 3 %)
+#pragma unroll
+          for (int h = 0; h < NT; ++h)
+#pragma unroll
+            for (int m = 0; m < kMt; ++m)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[h][m][i] = __fmul_rn(s[h][m][i], sc[h][i & 1] * ksc);
+        }
         uint32_t pb[kTerms][NT][kMt][2];
 #pragma unroll
         for (int h = 0; h < NT; ++h) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float f = sc[h][j] * ksc, ms = (m_run[h][j] == -INFINITY ? 0.f : m_run[h][j]) - kPBias;
-            // (one rounding of the difference, small where p is large)
+            const float f = coarse ? 1.f : sc[h][j] * ksc;
+            // (rounded up: never below the reference less the bias, nor above the reference)
+            const float ms = __fadd_ru(m_run[h][j] == -INFINITY ? 0.f : m_run[h][j], -kPBias);
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
 #pragma unroll

@@ -157,3 +157,30 @@ def test_fp32_query_elements_far_below_the_largest():
         e = 2.0 ** -25 * float(R.dense(kc, ks).abs().sum(-1).max()) * 0.2
         A = R.attention(q, kc, vc & 127, ks, vs, [S], 0.2)[0]
         R.within(out, ref, bound + math.expm1(2 * e) * A)
+
+
+def _average_of_rows(out, vc, vs, group, what):
+    """Every row lies between the least and the largest of V, but for the roundings of weights (fp16's
+    2^-11), their products and sums over S keys (a whole step each, twice) and of the result."""
+    v = R.dense(vc, vs)[0].repeat_interleave(group, 0)
+    lo, hi, x = v.amin(1), v.amax(1), out.cpu().double()
+    tol = hi * (R.HALF[out.dtype] + 2.0 ** -10 + v.shape[1] * 2.0 ** -22)
+    assert bool(((x >= lo - tol) & (x <= hi + tol)).all()), what
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("S", [700, 3000])  # an item whole, and cut into runs
+@pytest.mark.parametrize("nh,T", [(4, 1), (6, 5), (4, 30), (4, 100)])
+@pytest.mark.parametrize("size", [1e5, 1e7, 1e8, 1e10, 1e14])
+def test_attention_with_scores_whose_steps_are_large(dt, nh, T, size, S):
+    """Scores of 2^20 to 2^50 in powers of two: a step of fp32 there is up to 2^26, and a row is still
+    an average of V rows."""
+    hd, nkv = 128, 2
+    kc, vc, ks, vs = filled_cache(1, nkv, S, hd, 350)
+    R.append(vc, vs, 1 + 0.5 * randn(353, 1, S, nkv, hd).clamp(-1, 1), [0])
+    q = (size * randn(354, 1, T, nh, hd)).to(DT[dt])
+    out = torch.empty(1, T, nh, hd, dtype=DT[dt], device="cuda")
+    q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([S]).cuda(), 0.09)
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    R.within(out, ref, bound)
+    _average_of_rows(out[0], vc, vs, nh // nkv, size)
