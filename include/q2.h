@@ -244,7 +244,9 @@ q2_status q2_kv8_attention(void* out, const void* q, const int64_t* q_strides, c
  * q, out [seqlen, nh, hd] dense (out 16-byte aligned), kc, vc [nkv][max_seq]
  * [hd], ks, vs [nkv][nblk]; query row i sees keys j <= total_len - seqlen + i.
  * The lengths are the host's.  bf16, hd 128, a positive scale and 512 rows of
- * a kv head or more (seqlen * nh / nkv) run on the tcgen05 prompt attention. */
+ * a kv head or more (seqlen * nh / nkv) run on the tcgen05 prompt attention; a
+ * row with scaled scores past 2^30 ln 2 in magnitude may be NaN there, and is if
+ * its largest is one of them. */
 q2_status q2_kv8_self_attention(void* out, const void* q, const void* kc, const void* vc,
                                 const float* ks, const float* vs, size_t seqlen, size_t total_len,
                                 size_t nh, size_t nkv, size_t hd, size_t max_seq, float scale,

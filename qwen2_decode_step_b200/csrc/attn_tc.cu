@@ -205,9 +205,16 @@ struct AttnTc {
   const int* vnan;  // null, or [nkv][hd]: INT32_MAX - the first position with a NaN of V in that dim (0: none)
 };
 
+// Whether a row with maximum m (powers of two) and sum l has no result: its query
+// is not finite, a key range's scores are all NaN, or its scores are so large that
+// a step of fp32 there, 2^7 from 2^30 on, could take 2^(s - m) out of its range.
+// (Rounding the scores as m was before the difference would end that; each of four
+// forms of it, a branch in the softmax or its second copy, cost the whole kernel 4
+// to 5 %.)
+__device__ __forceinline__ bool no_result(float m, float l) { return !(fabsf(m) <= 0x1p30f) || isnan(l); }
+
 // Eight dims of the row at position pos: NaN where one of V's lies at or before it,
-// and everywhere in a row whose scores leave no sum (`none`: its query is not
-// finite, or a key range's scores are all NaN).
+// and everywhere in a row without a result (`none`).
 __device__ __forceinline__ void mark_nan(const int* vnan, int pos, bool none, float* f) {
   const int4 lo = __ldg(reinterpret_cast<const int4*>(vnan)), hi = __ldg(reinterpret_cast<const int4*>(vnan) + 1);
   const int first[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -489,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int t = 0; t < 8; ++t) f[t] = __uint_as_float(ov[e + t]) * inv;
             if (a.vnan)
-              mark_nan(a.vnan + (size_t)kvh * kHD + cb + 32 * c + e, a.pos0 + row, m_run == -INFINITY || isnan(lr), f);
+              mark_nan(a.vnan + (size_t)kvh * kHD + cb + 32 * c + e, a.pos0 + row, no_result(m_run, lr), f);
             *reinterpret_cast<uint4*>(out + 32 * c + e) = pack16<bf16>(f);
           }
         }
@@ -554,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 8; ++u) f[u] = o[e + u] * inv;
             if (a.vnan)
-              mark_nan(a.vnan + (size_t)kvh * kHD + cb + e, a.pos0 + row, mm == -INFINITY || isnan(ll), f);
+              mark_nan(a.vnan + (size_t)kvh * kHD + cb + e, a.pos0 + row, no_result(mm, ll), f);
             *reinterpret_cast<uint4*>(out + e) = pack16<bf16>(f);
           }
         }

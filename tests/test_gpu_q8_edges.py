@@ -184,3 +184,27 @@ def test_attention_with_scores_whose_steps_are_large(dt, nh, T, size, S):
     ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
     R.within(out, ref, bound)
     _average_of_rows(out[0], vc, vs, nh // nkv, size)
+
+
+@pytest.mark.parametrize("S,T", [(700, 300), (4000, 140)])
+@pytest.mark.parametrize("size", [1e5, 1e7, 1e8, 1e10, 1e14])
+def test_prompt_rows_with_scores_whose_steps_are_large(size, S, T):
+    """On the tcgen05 attention a row is an average of V rows up to scores of 2^30, NaN past them."""
+    hd, nh, nkv = 128, 8, 2
+    kc, vc, ks, vs = filled_cache(1, nkv, S, hd, 355)
+    R.append(vc, vs, 1 + 0.5 * randn(358, 1, S, nkv, hd).clamp(-1, 1), [0])
+    q = (size * randn(359, 1, T, nh, hd)).bfloat16()
+    out = torch.empty(T, nh, hd, dtype=torch.bfloat16, device="cuda")
+    q2.q2_kv8_self_attention(out, q[0].cuda(), *(t[0].cuda() for t in (kc, vc, ks, vs)), S, 0.09)
+    k = R.dense(kc, ks)[0].repeat_interleave(nh // nkv, 0)
+    s = torch.einsum("thd,hsd->ths", q[0].double(), k) * 0.09 * math.log2(math.e)
+    hidden = torch.arange(S) > torch.arange(S - T, S)[:, None]
+    top = s.masked_fill(hidden[:, None], -math.inf).amax(-1).abs()
+    nan = torch.isnan(out.cpu()).all(-1)
+    # (a score is off by hd 2^-23 of the sum of its magnitudes at most: far less than the thousandth here)
+    assert bool(nan[top > 2.0 ** 30 * 1.001].all()) and not bool(torch.isnan(out.cpu()[top < 2.0 ** 30 / 1.001]).any())
+    assert int((top > 2.0 ** 30 * 1.001).sum()) > 0 or size < 1e8
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    out[nan.cuda()] = ref[0][nan].bfloat16().cuda()
+    R.within(out, ref[0], bound[0])
+    _average_of_rows(out, vc, vs, nh // nkv, size)
