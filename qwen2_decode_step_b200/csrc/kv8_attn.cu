@@ -216,6 +216,14 @@ __device__ __forceinline__ void cta_sync() {
   __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
+// What a row's raw scores over a block are multiplied by: its own factor (>= 0)
+// times the scale of K, held to 2^120 (an infinity would make NaN of a score of 0;
+// NaN stays).
+__device__ __forceinline__ float score_factor(float row, float ksc) {
+  float f;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(row * ksc), "f"(0x1p120f));
+  return f;
+}
 // Which of the four codes of a word are NaN, as 0xff bytes.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t v) {
   return __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -387,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
   const int gq = lane >> 2, tq = lane & 3;
   const int G = a.group, rows = a.ntok * G;
   const int mi = lane >> 3, mr = lane & 7;
-  const float sl2 = a.scale * kLog2e;
+  const float sl2 = fabsf(a.scale) * kLog2e;  // (its sign goes to the query rows)
   // the slots of this warp's group (the nm warps of one kg), a ring; its first
   // warp fills them
   const int slots = kDepth * a.nm, slot0 = kg * slots;
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
       const int k = m > 0.f ? min(126, 127 + 8 - (int)(__float_as_uint(m) >> 23)) : 0;
       // (an infinite query leaves nothing but infinite and NaN scores: NaN, also
       // where all of them are -inf and no weight would be left)
-      const float up = m < INFINITY ? __uint_as_float((uint32_t)(127 + k) << 23) : NAN;
+      const float up = m < INFINITY ? copysignf(__uint_as_float((uint32_t)(127 + k) << 23), a.scale) : NAN;
       const float down = sl2 * __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll
       for (int j = 0; j < kW; ++j) {
@@ -679,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         for (int h = 0; h < NT; ++h)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float f = sc[h][j] * ksc;
+            const float f = score_factor(sc[h][j], ksc);
             float v[kMt][2];
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
@@ -736,14 +744,14 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[h][m][i] = __fmul_rn(s[h][m][i], sc[h][i & 1] * ksc);
+              for (int i = 0; i < 4; ++i) s[h][m][i] = __fmul_rn(s[h][m][i], score_factor(sc[h][i & 1], ksc));
         }
         uint32_t pb[kTerms][NT][kMt][2];
 #pragma unroll
         for (int h = 0; h < NT; ++h) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float f = coarse ? 1.f : sc[h][j] * ksc;
+            const float f = coarse ? 1.f : score_factor(sc[h][j], ksc);
             // (rounded up: never below the reference less the bias, nor above the reference)
             const float ms = __fadd_ru(m_run[h][j] == -INFINITY ? 0.f : m_run[h][j], -kPBias);
 #pragma unroll

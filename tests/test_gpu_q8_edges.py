@@ -208,3 +208,34 @@ def test_prompt_rows_with_scores_whose_steps_are_large(size, S, T):
     out[nan.cuda()] = ref[0][nan].bfloat16().cuda()
     R.within(out, ref[0], bound[0])
     _average_of_rows(out, vc, vs, nh // nkv, size)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("nh,T", [(4, 1), (6, 5), (4, 100), (4, 300)])
+def test_attention_where_the_scores_factor_leaves_the_range(dt, nh, T):
+    """Queries near the type's largest value over keys that are 0 there and large elsewhere; queries
+    near its smallest over keys near the largest."""
+    S, hd, nkv = 400, 128, 2
+    k = torch.zeros(1, S, nkv, hd)
+    k[..., 5] = 2.0 ** 30 * (1 + torch.rand(1, S, nkv, generator=torch.Generator().manual_seed(370)))
+    k[:, :, :, 9] = randn(371, 1, S, nkv) * 2.0 ** 29
+    kc, vc, ks, vs = empty_cache(1, nkv, S, hd)
+    R.append(kc, ks, k, [0])
+    R.append(vc, vs, randn(372, 1, S, nkv, hd), [0])
+    q = torch.zeros(1, T, nh, hd)
+    q[..., 0] = 2.0 ** 120                # scores of 0
+    q[:, :, 1, 0], q[:, :, 1, 9] = 0.0, 2.0 ** -28
+    q = q.to(DT[dt])
+    d = both(kc, vc, ks, vs)
+    out = torch.empty(1, T, nh, hd, dtype=DT[dt], device="cuda")
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    q2.q2_kv8_attention(out, q.cuda(), *d, i32([S]).cuda(), 0.09)
+    R.within(out, ref, bound, "batch")
+    q2.q2_kv8_self_attention(out[0], q[0].cuda(), *(t[0] for t in d), S, 0.09)
+    R.within(out, ref, bound, "rows")
+    # the other end
+    R.append(kc, ks, randn(373, 1, S, nkv, hd) * 2.0 ** 124, [0])
+    q = (randn(374, 1, T, nh, hd) * 2.0 ** -122).to(DT[dt])
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([S]).cuda(), 0.09)
+    R.within(out, ref, bound, "small queries")
