@@ -943,6 +943,9 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
 // CTA's groups where a few long sequences leave hundreds of parts (then the rows
 // are spread over gridDim.y), by one where a batch's items have two or three.
 constexpr int kJoinThreads = 256;
+// A part's sum is up to 2^14 for each of its keys: times this (it cancels) its
+// product with outputs near fp32's largest value stays in range.
+constexpr float kJoinScale = 0x1p-44f;
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a) {
   constexpr int kLanes = HD / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
@@ -995,7 +998,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a)
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (i0 + k * pg < n) {  // (no weight is skipped, as above)
-          const float e = w[k].y * ex2(w[k].x - ms);
+          const float e = w[k].y * kJoinScale * ex2(w[k].x - ms);
           W += e;
           y.x = fmaf(e, v[k].x, y.x);
           y.y = fmaf(e, v[k].y, y.y);

@@ -239,3 +239,16 @@ def test_attention_where_the_scores_factor_leaves_the_range(dt, nh, T):
     ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
     q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([S]).cuda(), 0.09)
     R.within(out, ref, bound, "small queries")
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("nh,T", [(4, 1), (6, 5), (2, 40)])
+def test_parts_of_values_near_the_largest_are_joined(dt, nh, T):
+    S, hd, nkv = 3000, 64, 2
+    kc, vc, ks, vs = filled_cache(1, nkv, S, hd, 375, spread=0.5)
+    R.append(vc, vs, 2.0 ** 126 * randn(379, 1, S, nkv, hd).clamp(-1.9, 1.9), [0])
+    q = randn(379, 1, T, nh, hd).to(DT[dt])
+    out = torch.empty(1, T, nh, hd, dtype=DT[dt], device="cuda")
+    q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([S]).cuda(), 0.125)
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.125)
+    R.within(out, ref, bound)
