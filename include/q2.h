@@ -230,7 +230,9 @@ q2_status q2_kv8_read(void* k, void* v, const void* kc, const void* vc, const fl
  * length <= 0, or lens[b] < ntok) is zero; lens[b] past max_seq: zero rows and
  * Q2_ERR_CAPACITY in the device error word.  Codes and scales past lens[b] may
  * hold anything.  A query row that is not finite, or sees a NaN of K, is NaN in
- * every dimension, one that sees a NaN of V in that dimension.  nh / nkv <= 8.
+ * every dimension, one that sees a NaN of V in that dimension.  bf16: a block of
+ * V whose scale lies 2^80 or more below another's of its head may count as less
+ * than it is.  nh / nkv <= 8.
  * workspace: device memory of at least q2_kv8_attention_workspace() bytes,
  * 256-byte aligned, contents ignored (NULL where that is 0); calls that may
  * overlap on the GPU need one each. */

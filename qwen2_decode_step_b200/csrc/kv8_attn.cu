@@ -646,12 +646,16 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
               for (int i = 0; i < 4; ++i) s[0][m][i] += s2[m][i];
           }
         }
-        // ---- the unit of this block's V scale (never 2^60 below the largest so
-        // far: the output in units of it stays in range)
+        // ---- the unit of the output from this block on: its V scale, within what
+        // keeps all that was added in other units in range.  A block whose scale lies
+        // outside adds its products times `apart`: fp32 to the sums, any scales; bf16
+        // by way of the probabilities, where it loses bits from 2^-20 on (products of
+        // their own took the registers of four row tiles: 336 bytes spilled).
         unit_max = fmaxf(unit_max, vsc);
-        const float unit_new = fmaxf(fmaxf(vsc, unit_max * 0x1p-60f), 0x1p-126f);
+        const float unit_new = kWide ? fminf(fmaxf(fmaxf(vsc, unit_max * 0x1p-60f), 0x1p-60f), 0x1p50f)
+                                     : fmaxf(fmaxf(vsc, unit_max * 0x1p-80f), 0x1p-60f);
         const float ratio = unit_new == unit ? 1.f : unit / unit_new;
-        const float pf = vsc == unit_new ? 1.f : vsc / unit_new;
+        const float apart = vsc == unit_new ? 1.f : vsc / unit_new;
         unit = unit_new;
         const bool edge = key0 + kKeys > clear;
         // ---- rows past the sequence, NaN that not every row sees
@@ -768,11 +772,11 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
             const float sum = (s[h][0][j] + s[h][0][2 + j]) + (s[h][1][j] + s[h][1][2 + j]);
             l_run[h][j] += sum;
           }
-          if (pf != 1.f) {
+          if (!kWide && apart != 1.f) {
 #pragma unroll
             for (int m = 0; m < kMt; ++m)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[h][m][i] *= pf;
+              for (int i = 0; i < 4; ++i) s[h][m][i] *= apart;
           }
 #pragma unroll
           for (int m = 0; m < kMt; ++m)
@@ -805,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
                 mma_f16(low, va, pb[kTerms - 1][h][kk][0], pb[kTerms - 1][h][kk][1]);
                 mma_f16(t, va, pb[0][h][kk][0], pb[0][h][kk][1]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[h][c][j] += fmaf(low[j], 1.f / kLow, t[j]);
+                for (int j = 0; j < 4; ++j) o[h][c][j] = fmaf(fmaf(low[j], 1.f / kLow, t[j]), apart, o[h][c][j]);
               } else {
                 mma_f16(o[h][c], va, pb[0][h][kk][0], pb[0][h][kk][1]);
               }

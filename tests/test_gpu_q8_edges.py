@@ -252,3 +252,31 @@ def test_parts_of_values_near_the_largest_are_joined(dt, nh, T):
     q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([S]).cuda(), 0.125)
     ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.125)
     R.within(out, ref, bound)
+
+
+@pytest.mark.parametrize("T", [1, 5, 12, 40, 130])
+@pytest.mark.parametrize("dt,large,small", [
+    ("bf16", 1.0, 2.0 ** -64), ("bf16", 2.0 ** 20, 2.0 ** -57), ("bf16", 2.0 ** 100, 2.0 ** 25),
+    ("f32", 1.0, 2.0 ** -64), ("f32", 2.0 ** 110, 2.0 ** -40), ("f32", 2.0 ** 100, 2.0 ** 35),
+    ("f32", 2.0 ** 124, 2.0 ** -55)])
+def test_attention_to_small_values_beside_large_ones(dt, T, large, small):
+    """Every other query row sees, for all its weight is worth, the small blocks alone."""
+    S, hd, nh, nkv = 64 * 6, 64, 2, 2
+    which = torch.tensor([1, 0, 0, 1, 0, 1]).repeat_interleave(64)   # 1: a block of small values
+    k = torch.zeros(1, S, nkv, hd)
+    k[0, :, :, 0] = torch.where(which == 1, 4.0, -4.0)[:, None]
+    k[..., 1:] = 0.05 * randn(380, 1, S, nkv, hd - 1)
+    v = randn(381, 1, S, nkv, hd) * torch.where(which == 1, small, large)[None, :, None, None]
+    kc, vc, ks, vs = empty_cache(1, nkv, S, hd)
+    R.append(kc, ks, k, [0])
+    q = randn(382, 1, T, nh, hd)
+    q[0, :, :, 0] = 90.0
+    q[0, 1::2, :, 0] = -90.0
+    q = q.to(DT[dt])
+    for values in (v, v.flip(1)):
+        R.append(vc, vs, values, [0])
+        out = torch.empty(1, T, nh, hd, dtype=DT[dt], device="cuda")
+        for n in (S, 130):
+            q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([n]).cuda(), 1.0)
+            ref, bound = R.attention(q, kc, vc, ks, vs, [n], 1.0)
+            R.within(out, ref, bound)
