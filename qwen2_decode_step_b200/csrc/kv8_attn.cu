@@ -66,6 +66,9 @@ constexpr float kPBias = 6.f, kGrow = 8.f;      // p <= 2^(6 + 8) in fp16, see s
 // from it, so that the difference is exact and the bound on p holds (below it one
 // rounding of the difference, small where p is large).
 constexpr float kCoarse = 0x1p20f;
+// A part's sum is up to 2^14 for each of its keys: times this (it cancels) its
+// product with outputs near fp32's largest value stays in range in the join.
+constexpr float kPartScale = 0x1p-44f;
 // fp32: the low fp16 part of a query element or probability is kept times kLow, in
 // sums of its own, so that fp16's smallest step, 2^-24, costs 2^-37 and not 2^-25
 // (a key holding nearly all weight over 32767 others of 2^-31 each: they were lost
@@ -89,7 +92,7 @@ struct Kv8Attn {
   int mgroups;  // items of a (sequence, kv head)
   float scale;
   void* out;    // [batch][ntok][nh][hd]
-  float* part;  // [2 * CTAs][irows][hd + 2]: rows of partial items, then m and l of each row
+  float* part;  // [2 * CTAs][irows][hd + 2]: rows of partial items, then m and l 2^-44 of each row
   int4* cut;    // [items]: how the runs cut each item
   int ctas;     // of the split kernel
   int whole;    // a CTA per item, nothing is cut (see split_plan)
@@ -900,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
         if (k < kw) MLw[2 * (tid + kRows * a.nm * k)] = ml[k].y * inv;
       if (!whole)
         *reinterpret_cast<float2*>(a.part + (size_t)2 * a.ctas * a.irows * HD + 2 * ((size_t)part * a.irows + tid)) =
-            make_float2(M, W);
+            make_float2(M, W * kPartScale);
     }
     if (tid == 0 && w.at == 0 && !a.whole)
       a.cut[w.e * a.nkv + w.g] = make_cut((u + w.nu - 1) / run - (int)blockIdx.x + 1, blockIdx.x, u != u0 ? 1 : 0);
@@ -947,9 +950,6 @@ __global__ void __launch_bounds__(kThreads, SplitSmem<HD, NT>::kCtas)
 // CTA's groups where a few long sequences leave hundreds of parts (then the rows
 // are spread over gridDim.y), by one where a batch's items have two or three.
 constexpr int kJoinThreads = 256;
-// A part's sum is up to 2^14 for each of its keys: times this (it cancels) its
-// product with outputs near fp32's largest value stays in range.
-constexpr float kJoinScale = 0x1p-44f;
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a) {
   constexpr int kLanes = HD / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
@@ -1002,7 +1002,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(const Kv8Attn a)
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (i0 + k * pg < n) {  // (no weight is skipped, as above)
-          const float e = w[k].y * kJoinScale * ex2(w[k].x - ms);
+          const float e = w[k].y * ex2(w[k].x - ms);
           W += e;
           y.x = fmaf(e, v[k].x, y.x);
           y.y = fmaf(e, v[k].y, y.y);
