@@ -279,7 +279,9 @@ q2_status q2_quantize_q8(void* codes, float* scales, const void* in, size_t rows
  * (sum over k in g of xq[m, k] * wq[n, k]) + bias[n]; xq [M, K] and xs from
  * quantize_q8 with block_rows 1, wq [N, K] and ws with block_rows 128, both
  * codes 16-byte aligned, K a multiple of 16; bias [N] or NULL and out [M, N] in
- * `dtype`; fp32 sums, one rounding. */
+ * `dtype`; fp32 sums, one rounding.  The two scales of a group are multiplied
+ * first: a product below 2^-126 loses bits, one past fp32's largest value is held
+ * to it. */
 q2_status q2_linear_q8(void* out, const void* xq, const float* xs, const void* wq, const float* ws,
                        const void* bias, size_t M, size_t N, size_t K, int dtype, void* stream);
 

@@ -280,3 +280,46 @@ def test_attention_to_small_values_beside_large_ones(dt, T, large, small):
             q2.q2_kv8_attention(out, q.cuda(), *both(kc, vc, ks, vs), i32([n]).cuda(), 1.0)
             ref, bound = R.attention(q, kc, vc, ks, vs, [n], 1.0)
             R.within(out, ref, bound)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("M,N,K", [(1, 200, 512), (5, 140, 400), (30, 130, 640), (64, 260, 384), (70, 130, 512),
+                                   (130, 8200, 400), (2500, 3000, 272), (2500, 3001, 512)])
+def test_linear_with_scales_near_the_ends_of_the_range(dt, M, N, K):
+    """Scales whose product passes fp32's largest value over a group that sums to 0, and products near
+    both ends of the normal range."""
+    g = torch.Generator().manual_seed(360)
+    xq = torch.randint(0, 127, (M, K), generator=g, dtype=torch.uint8)
+    wq = torch.randint(0, 127, (N, K), generator=g, dtype=torch.uint8)
+    G, NB = -(-K // 128), -(-N // 128)
+    xs, ws = torch.ones(G, M), torch.ones(NB, G)
+    # group 0: 1e19 x 1e20, nothing but zeros
+    xq[::2, :128], wq[:, :128] = 0, 0
+    xs[0], ws[:, 0] = 1e19, 1e20
+    xs[0, 2::4], ws[NB - 1, 0] = -1e19, -1e20
+    # group 1: 1e18 x 1e19, one product of the smallest codes or none
+    xq[:, 128:256], wq[:, 128:256] = 0, 0
+    xq[:, 133], wq[::2, 133] = 1, 129
+    xs[1], ws[:, 1] = 1e18, 1e19
+    # the last group: 1e-19 x 1e-18, all that every third row has
+    xs[G - 1], ws[:, G - 1] = 1e-19, 1e-18
+    xs[:G - 1, ::3] = 0.0
+    out = torch.empty(M, N, dtype=DT[dt], device="cuda")
+    q2.q2_linear_q8(out, *both(xq, xs, wq, ws))
+    ref, bound = R.linear(xq, xs, wq, ws, None, DT[dt])
+    R.within(out, ref, bound)
+
+
+@pytest.mark.parametrize("M", [3, 130])
+def test_linear_scales_that_are_not_finite_reach_their_results(M):
+    N, K = 140, 256
+    xq, xs = R.quantise(randn(365, M, K), 1)
+    wq, ws = R.quantise(randn(366, N, K), 128)
+    xs[0, 0], xs[1, 1], ws[1, 1] = math.nan, math.inf, -math.inf
+    out = torch.empty(M, N, device="cuda")
+    q2.q2_linear_q8(out, *both(xq, xs, wq, ws))
+    got = out.cpu()
+    assert bool(torch.isnan(got[0]).all())
+    assert not bool(torch.isfinite(got[1]).any()) and not bool(torch.isfinite(got[2:, 128:]).any())
+    ref, bound = R.linear(xq[2:], xs[:, 2:], wq[:128], ws[:1], None, torch.float32)
+    R.within(got[2:, :128], ref, bound)
