@@ -323,3 +323,21 @@ def test_linear_scales_that_are_not_finite_reach_their_results(M):
     assert not bool(torch.isfinite(got[1]).any()) and not bool(torch.isfinite(got[2:, 128:]).any())
     ref, bound = R.linear(xq[2:], xs[:, 2:], wq[:128], ws[:1], None, torch.float32)
     R.within(got[2:, :128], ref, bound)
+
+
+@pytest.mark.parametrize("dt", DT)
+@pytest.mark.parametrize("T", [1, 4])
+def test_a_sequence_is_the_same_alone_and_beside_others(dt, T):
+    """Where its keys are cut depends on its neighbours' lengths; its rows stay within the bound."""
+    S, hd, nh, nkv = 3000, 128, 12, 2
+    kc, vc, ks, vs = filled_cache(6, nkv, S, hd, 390, spread=0.7)
+    q = randn(394, 6, T, nh, hd).to(DT[dt])
+    scale = 1.0 / math.sqrt(hd)
+    lens = [1555, 3000, 17, T, 2900, 640]
+    ref, bound = R.attention(q, kc, vc, ks, vs, lens, scale)
+    d = both(q, kc, vc, ks, vs)
+    for batch in ([0], [4], [5], [0, 1, 4], [4, 2, 3], [3, 3, 5, 3], [1, 2, 0, 3, 5, 4]):
+        at = torch.tensor(batch, device="cuda")
+        out = torch.empty(len(batch), T, nh, hd, dtype=DT[dt], device="cuda")
+        q2.q2_kv8_attention(out, *(t[at].contiguous() for t in d), i32([lens[b] for b in batch]).cuda(), scale)
+        R.within(out, ref[at.cpu()], bound[at.cpu()], batch)
