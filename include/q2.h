@@ -68,10 +68,11 @@ const char* q2_version(void);
 
 /* Synchronises `stream`, then reports what the per-operator kernels on the
  * current device recorded since the last check, and clears the record:
- * Q2_ERR_TIMEOUT if a bounded wait inside a kernel ran out (the tcgen05 GEMM
- * behind q2_linear), else Q2_ERR_INDEX if a kernel saw a token id outside
- * the vocabulary, else Q2_ERR_CAPACITY if a call on an 8-bit cache saw a
- * length past max_seq, else Q2_OK. */
+ * Q2_ERR_TIMEOUT if a bounded wait inside a kernel ran out (those behind
+ * q2_linear, q2_self_attention, q2_linear_q8 and the 8-bit cache's attention),
+ * else Q2_ERR_INDEX if a kernel saw a token id outside the vocabulary, else
+ * Q2_ERR_CAPACITY if a call on an 8-bit cache saw a length past max_seq, else
+ * Q2_OK. */
 q2_status q2_check_device_error(void* stream);
 
 /* Test hook: ORs `bits` (1: out-of-range id, 2: wait ran out) into the
@@ -226,8 +227,11 @@ q2_status q2_kv8_read(void* k, void* v, const void* kc, const void* vc, const fl
  * the positions held, the ntok new ones included; query row t of sequence b
  * sees keys j <= lens[b] - ntok + t.  q [batch, ntok, nh, hd] (the nh * hd
  * elements of a token contiguous; q_strides as k_strides above), out dense and
- * 16-byte aligned; scores, softmax and sums in fp32.  A row that sees no key (a sequence of
- * length <= 0, or lens[b] < ntok) is zero; lens[b] past max_seq: zero rows and
+ * 16-byte aligned.  Scores, softmax and sums are fp32; a probability enters its
+ * product with V as one fp16 (bf16 inputs), as two bf16 parts (bf16 on the prompt
+ * path below) or as two fp16 parts (fp32: to 2^-22 of itself or 2^-43 of the
+ * row's largest).  A row that sees no key (a sequence of length <= 0, or
+ * lens[b] < ntok) is zero; lens[b] past max_seq: zero rows and
  * Q2_ERR_CAPACITY in the device error word.  Codes and scales past lens[b] may
  * hold anything.  A query row that is not finite, or sees a NaN of K, is NaN in
  * every dimension, one that sees a NaN of V in that dimension.  bf16: a block of

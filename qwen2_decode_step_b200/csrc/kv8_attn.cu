@@ -5,13 +5,14 @@
 // the query rows of a kv head (ntok rows x nh / nkv heads) on N, eight a tile:
 // S^T = K q^T, O^T = V^T P^T.  A decode step's at most eight rows fill one
 // tile; with the rows on M half of every MMA and of the accumulators stood
-// empty.  A warp takes NT row tiles (one, or two where there are more than
-// eight rows), up to four warps the rows of a work item (sequence, row group, kv
-// head); its unit of work is 32 keys, half a block.  All items' units, in
-// order, are dealt to a grid of resident CTAs in equal runs (lengths are read
-// on the device), so ragged batches and a single long sequence load every SM
-// alike; an item cut by a run's end leaves partial results that a second kernel
-// joins in order (the same result every time).
+// empty.  A warp takes NT row tiles (one, two from nine rows on, in bf16 four from
+// 65 on), up to four warps the rows of a work item (sequence, row group, kv head);
+// its unit of work is 32 keys, half a block.  All items' units, in order, are dealt
+// to a grid of resident CTAs in equal runs (lengths are read on the device), so
+// ragged batches and a single long sequence load every SM alike; an item cut by a
+// run's end leaves partial results that a second kernel joins in order (the same
+// result every time).  Short items, and items in plenty, go to a CTA each instead:
+// one launch, nothing to join (split_plan).
 //
 // Bound by HBM (a byte per cached element): a unit's K and V rows arrive by TMA
 // (swizzled to the head's row length) in slots of their own for each group of
@@ -24,25 +25,30 @@
 //   output  ldmatrix.trans on byte pairs gives a lane two keys x two dims; one
 //           byte permute splits them into rows g (even dims) and g + 8 (odd) of
 //           the A operand.  P turns from the scores' layout by movmatrix.
-// The query rows are scaled by a power of two into fp16's range (exact for
-// bf16; fp32 queries are split into a high and a low fp16 part, two MMAs, and
-// so are their probabilities).  Softmax in fp32, online, with p = 2^(s - m + 6),
-// m the row's reference: the largest score when it was last taken.  It is taken
-// again (shuffles over the eight lanes that hold a row's keys, the output
-// rescaled) only when a score passes it by 8, so that most units need one vote;
-// the common factor cancels, p stays below 2^14 and probabilities down to 2^-20
-// of the largest keep fp16's full 11 bits.  The scale of K multiplies the scores; the
-// output is accumulated in units of the current block's V scale and moved to
-// the next block's where that differs (a power of two: exact).
+// The query rows are scaled by a power of two so that their largest element lies in
+// [256, 512): a bf16 element is then exact in fp16 from 2^-25 of the largest on and
+// within 2^-33 of the largest below that; an fp32 element is a high and a low fp16
+// part (two MMAs) to 2^-22 of itself, and so is an fp32 row's probability (see kLow).
+// Softmax in fp32, online, with p = 2^(s - m + 6), m the row's reference: the
+// largest score when it was last taken.  It is taken again (shuffles over the eight
+// lanes that hold a row's keys, the output rescaled) only when a score passes it by
+// 8, so that most units need one vote; the common factor cancels.  p stays below
+// 2^14.  A bf16 row's p is one fp16, as the output keeps 8 bits and its sums average
+// the roundings: 11 bits down to 2^-20 of the largest, then to within 2^-31 of it (a
+// second part would double the output's MMAs; over the decode batch the error
+// against 64 bits is 0.0017, as a plain fp32 computation's: the output's rounding).
+// The scale of K multiplies
+// the scores; the output is accumulated in units of the current block's V scale and
+// moved to the next block's where that differs (a power of two: exact).
 //
 // Prompt rows (bf16, head dim 128, 512 rows of a kv head or more): the cache's K and
 // V are read back to bf16 (exact) in the workspace and the prompt attention on
 // tcgen05 runs over them.  That product is bound by the tensor core: the copy
 // moves 6 bytes per cached element once, against 4 rows x heads operations per
-// element (4096 rows over 32768 keys: 882 us, 877
-// TFLOP/s, some 10 of them the copy).  A NaN of
-// V, which the zero probabilities of rows that do not see it would spread, is
-// taken out of the copy and put into the rows that do see it at the end.
+// element (4096 rows over 32768 keys, 12 / 2 heads: 1003 us in steady calls, 771
+// TFLOP/s, 11 of them the copy).  A NaN of V, which the zero probabilities of rows
+// that do not see it would spread, is taken out of the copy and put into the rows
+// that do see it at the end.
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "kernels.h"
@@ -61,8 +67,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCtasMax = 512;
 constexpr float kPBias = 6.f, kGrow = 8.f;      // p <= 2^(6 + 8) in fp16, see softmax
-// References above this (in powers of two) lie a sixteenth or more off their own
-// exact product: from here on every score is rounded before the reference is taken
+// References above this (in powers of two) may lie a sixteenth and more off their
+// own exact product: from here on every score is rounded before the reference is taken
 // from it, so that the difference is exact and the bound on p holds (below it one
 // rounding of the difference, small where p is large).
 constexpr float kCoarse = 0x1p20f;
@@ -1102,8 +1108,10 @@ SplitPlan split_plan(size_t batch, size_t ntok, size_t nh, size_t nkv, size_t hd
   if (p.ctas > kCtasMax) p.ctas = kCtasMax;
   // Items whole: no scan of the lengths, nothing to join, one launch, no
   // workspace.  Where a warp has at most six units of an item to itself (12 / 2
-  // heads, us with / without: 64 sequences in caches of 512 positions 8.6 / 13.6,
-  // of 1000 12.6 / 14.9, of 2000 21.7 / 20.0), and where items by far outnumber the
+  // heads, us on the GPU with / without: one sequence in a cache of 128 positions
+  // 4.5 / 6.8, of 577 9.2 / 11.8, of 760 10.3 / 8.4; 4 of 577 9.2 / 12.1, of 760
+  // 10.3 / 12.2; 16 of 760 10.3 / 13.5; 64 of 300 8.0 / 14.4, of 760 12.1 / 16.2, of
+  // 2000 21.7 / 20.0: past the rule), and where items by far outnumber the
   // resident CTAs and are not so long that the last ones leave the machine idle
   // (128 sequences x 8 heads: ragged up to 2000 positions 43 / 55, of 2000 each 62
   // / 62, of 6000 each 155 / 141).
@@ -1138,8 +1146,8 @@ bool use_tc(size_t ntok, size_t group, size_t hd, int dtype) {
   return dtype == Q2_BF16 && hd == 128 && ntok >= 16 && ntok * group >= kTcRows;
 }
 
-// Workspace: the tcgen05 attention's counters and, next to them, the NaN words
-// (one memset clears both), its slots, K, V.
+// Workspace: the tcgen05 attention's counters and slots, the NaN words (a memset
+// clears the counters, another these), K, V.
 struct TcPlan {
   size_t nan, k, v, bytes;
 };

@@ -298,7 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kV = Storage<T>::kVec;
     // Weight scales: of 256 columns by lane (32 groups' lie next to each other, a
     // lane reads one and hands it to the others at its group), and the loop in steps
-    // of one group; 4096 x 17920 x 1536 131 -> 118 us, x 4096 308 -> 292.  Of fewer
+    // of one group; 4096 x 17920 x 1536 131 -> 118 us (short runs; 139 in steady
+    // calls, under the power limit), x 4096 308 -> 292.  Of fewer
     // columns by every lane at each group, in steps of two: by lane 192 columns
     // took 74-80 us instead of 65-72 (4096 x 1536 x 8960), 128 columns 32 instead
     // of 30 (1000 x 4096 x 4096 fp32), 64 tokens the same.
