@@ -467,6 +467,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(0u, 0u, 0u, 0u);
         }
       }
+      // The last tile: the product of the tile before is waited for while this one
+      // cannot have run yet.  A row group may be a tile ahead of the others, and the
+      // wait for the last product below tells phases by their parity alone: with two
+      // of them open it would take the one before the last two for its own.
+      if (j > 0 && j == n - 1 && !wait_bar(o_done, (uint32_t)((j - 1) & 1))) atomicOr(a.err, 2);
       fence_proxy_async_smem();  // the exchange and zeroed V rows: the async proxy refills or reads them next
       fence_before();
       mbar_arrive(&p_full[s]);

@@ -341,3 +341,24 @@ def test_a_sequence_is_the_same_alone_and_beside_others(dt, T):
         out = torch.empty(len(batch), T, nh, hd, dtype=DT[dt], device="cuda")
         q2.q2_kv8_attention(out, *(t[at].contiguous() for t in d), i32([lens[b] for b in batch]).cuda(), scale)
         R.within(out, ref[at.cpu()], bound[at.cpu()], batch)
+
+
+@pytest.mark.parametrize("S,T,nh,nkv", [(300, 140, 8, 2), (900, 130, 8, 2), (1000, 140, 8, 2), (2000, 140, 8, 2),
+                                        (3000, 128, 8, 2), (4000, 140, 8, 2), (4000, 129, 6, 3), (4096, 512, 2, 2)])
+def test_prompt_rows_cut_into_short_key_ranges(S, T, nh, nkv):
+    """Few row blocks over a long cache: a CTA has one to six key tiles, and a row group of it may run
+    a tile ahead of the others.  The dense attention shares the kernel."""
+    kc, vc, ks, vs = filled_cache(1, nkv, S, 128, 410, spread=0.5)
+    R.append(vc, vs, 1 + 0.5 * randn(413, 1, S, nkv, 128).clamp(-1, 1), [0])
+    q = randn(414, 1, T, nh, 128).bfloat16()
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    d = [t[0].cuda() for t in (kc, vc, ks, vs)]
+    k, v = (R.dense(c, s)[0].transpose(0, 1).bfloat16().contiguous().cuda() for c, s in ((kc, ks), (vc, vs)))
+    qd = q[0].cuda()
+    outs = torch.empty(2, 6, T, nh, 128, dtype=torch.bfloat16, device="cuda")
+    for i in range(6):
+        q2.q2_kv8_self_attention(outs[0, i], qd, *d, S, 0.09)
+        q2.q2_self_attention(outs[1, i], qd, k, v, 0.09)
+    R.within(outs[0, 0], ref[0], bound[0], "8-bit cache")
+    R.within(outs[1, 0], ref[0], bound[0], "dense")
+    assert torch.equal(outs, outs[:, :1].expand_as(outs))
