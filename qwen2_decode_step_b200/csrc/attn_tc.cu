@@ -584,8 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // K/V either head-major (positions of one kv head contiguous, the cache's
 // layout: [nkv][positions][hd]) or token-major (the heads of one position
-// contiguous: [positions][nkv][hd]).
-static bool kv_head_major(const AttnRows& a) { return a.kv_tok_stride == kHD && a.kv_head_stride % kHD == 0; }
+// contiguous: [positions][nkv][hd]).  With one kv head the second may look like the
+// first with one position a head.
+static bool kv_head_major(const AttnRows& a) {
+  return a.kv_tok_stride == kHD && a.kv_head_stride % kHD == 0 && a.kv_head_stride > kHD;
+}
 static bool kv_token_major(const AttnRows& a) {
   return a.kv_head_stride == kHD && a.kv_tok_stride % 8 == 0 && a.kv_tok_stride >= (long long)a.nkv * kHD;
 }

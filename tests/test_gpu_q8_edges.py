@@ -362,3 +362,14 @@ def test_prompt_rows_cut_into_short_key_ranges(S, T, nh, nkv):
     R.within(outs[0, 0], ref[0], bound[0], "8-bit cache")
     R.within(outs[1, 0], ref[0], bound[0], "dense")
     assert torch.equal(outs, outs[:, :1].expand_as(outs))
+
+
+@pytest.mark.parametrize("S,T,nh", [(16, 16, 1), (17, 17, 8), (130, 128, 1), (700, 300, 6), (2000, 140, 8)])
+def test_dense_self_attention_with_one_kv_head(S, T, nh):
+    kc, vc, ks, vs = filled_cache(1, 1, S, 128, 420, spread=0.5)
+    q = randn(424, 1, T, nh, 128).bfloat16()
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    k, v = (R.dense(c, s)[0].transpose(0, 1).bfloat16().contiguous().cuda() for c, s in ((kc, ks), (vc, vs)))
+    out = torch.empty(T, nh, 128, dtype=torch.bfloat16, device="cuda")
+    q2.q2_self_attention(out, q[0].cuda(), k, v, 0.09)
+    R.within(out, ref[0], bound[0])
