@@ -202,6 +202,7 @@ struct AttnTc {
   int ts;        // the later items' key ranges (CTA n_whole + p: range p / n_tail of item n_whole + p % n_tail)
   float* part;   // [n_tail * ts] slots of kSlotFloats
   int* cnt;      // [n_tail] ranges done (0 between launches)
+  float out_mul;    // of the output: undoes V's factor
   const int* vnan;  // null, or [nkv][hd]: INT32_MAX - the first position with a NaN of V in that dim (0: none)
 };
 
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = q0 + r;
     bf16* out = reinterpret_cast<bf16*>(a.out) + (size_t)row * a.out_row_stride + (size_t)h * kHD + cb;
     if (piece < 0) {
-      const float inv = lr > 0.f ? 1.f / lr : 0.f;
+      const float inv = lr > 0.f ? a.out_mul / lr : 0.f;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
         uint32_t ov[32];
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[4 * d + 3] += w * v.w;
           }
         }
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float inv = ll > 0.f ? a.out_mul / ll : 0.f;
         if (row < a.rows) {
 #pragma unroll
           for (int e = 0; e < 64; e += 8) {
@@ -696,6 +697,7 @@ q2_status launch_attn_tc_nan(const AttnRows& a, void* ws, int* err, cudaStream_t
   p.out_row_stride = a.out_row_stride;
   p.err = err;
   p.vnan = vnan;
+  p.out_mul = vnan ? 1.f / kKv8VFactor : 1.f;
   p.ntq = (a.rows + kQB - 1) / kQB;
   const int items = p.ntq * a.nh;
   attn_tc_plan(a.rows, pos0, a.nh, num_sms(), ws != nullptr, &p.n_whole, &p.ts);

@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kThreads) kv8_read_kernel(const Kv8Read a, int
   uint2 w[kPer];
   // the tile's 64 positions lie in two blocks at most
   const int b0 = (start + t0) / kBlk, split = (b0 + 1) * kBlk - start - t0;  // rows of the tile in the first
-  const float s0 = __ldg(scale + b0), s1 = __ldg(scale + min(b0 + 1, nblk - 1));
+  const float by = isv && a.vnan ? kKv8VFactor : 1.f;
+  const float s0 = __ldg(scale + b0) * by, s1 = __ldg(scale + min(b0 + 1, nblk - 1)) * by;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int it = threadIdx.x + i * kThreads;

@@ -373,3 +373,19 @@ def test_dense_self_attention_with_one_kv_head(S, T, nh):
     out = torch.empty(T, nh, 128, dtype=torch.bfloat16, device="cuda")
     q2.q2_self_attention(out, q[0].cuda(), k, v, 0.09)
     R.within(out, ref[0], bound[0])
+
+
+@pytest.mark.parametrize("S,T", [(700, 300), (4000, 140)])  # whole items, and key ranges that are merged
+@pytest.mark.parametrize("size", [2.0 ** 126, 2.0 ** -62])
+def test_prompt_rows_over_values_near_the_ends_of_the_range(size, S, T):
+    hd, nh, nkv = 128, 8, 2
+    kc, vc, ks, vs = filled_cache(1, nkv, S, hd, 400, spread=0.5)
+    v = randn(404, 1, S, nkv, hd).clamp(-1.9, 1.9)
+    v[..., ::3] = v[..., ::3].abs()
+    R.append(vc, vs, size * v, [0])
+    vc[0, 1, S - 100, 9] = 127
+    q = randn(405, 1, T, nh, hd).bfloat16()
+    out = torch.empty(T, nh, hd, dtype=torch.bfloat16, device="cuda")
+    q2.q2_kv8_self_attention(out, q[0].cuda(), *(t[0].cuda() for t in (kc, vc, ks, vs)), S, 0.09)
+    ref, bound = R.attention(q, kc, vc, ks, vs, [S], 0.09)
+    R.within(out, ref[0], bound[0])
