@@ -359,11 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qpos = a.pos0 + q0 + r;        // this row sees keys 0 .. qpos
     const float sl2 = a.scale * kLog2e;
     // the two warps of a row group meet on their own named barrier (1 + rg, 64 threads)
-    auto pair_sync = [rg] { asm volatile("bar.sync %0, 64;" ::"r"(1 + rg) : "memory"); };
+    // (these barriers and the tensor-memory accesses take whole warps; a wait, which
+    // each lane does for itself, may leave a warp apart)
+    auto pair_sync = [rg] {
+      __syncwarp();
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + rg) : "memory");
+    };
     float m_run = -INFINITY, l_run = 0.f;
     for (int j = 0; j < n; ++j) {
       const int s = j & 1, kv = j % kStages;
       if (!wait_bar(&s_full[s], (uint32_t)((j >> 1) & 1))) atomicOr(a.err, 2);
+      __syncwarp();
       fence_after();
       // This warp's half of the row's raw scores, kept in registers for both
       // passes; keys beyond the row's position become -inf (only on the
@@ -414,6 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O is rescaled once the product of the tile before is done
         if (!wait_bar(o_done, (uint32_t)((j - 1) & 1))) atomicOr(a.err, 2);
+        __syncwarp();
         fence_after();
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
@@ -481,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // slot): the two halves' sums are added through the Q buffer (free once
     // every product is done)
     if (n > 0 && !wait_bar(o_done, (uint32_t)((n - 1) & 1))) atomicOr(a.err, 2);
+    __syncwarp();
     fence_after();
     float* lx = reinterpret_cast<float*>(smem + kQOff);
     lx[half * kQB + r] = l_run;
@@ -531,6 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (done == a.ts - 1) a.cnt[t] = 0;  // every range has counted: ready for the next launch
         *last = done == a.ts - 1;
       }
+      __syncwarp();
       asm volatile("bar.sync 5, 256;" ::: "memory");
       if (*last) {
         __threadfence();
